@@ -84,9 +84,12 @@ const char* convrot_status_string(convrot_status st);
 /*
  * Reads and clears the device error word after synchronising `stream`.
  * Returns CONVROT_OK if no kernel has reported a problem since the last call,
- * CONVROT_ERR_DEVICE_TIMEOUT if one gave up on a bounded wait, or
- * CONVROT_ERR_CUDA if the synchronisation itself failed.  If detail is not
- * NULL it receives the raw error word (0 when clean).
+ * CONVROT_ERR_DEVICE_TIMEOUT if one gave up on a bounded wait (bit 0),
+ * CONVROT_ERR_SHAPE if the only problem was an index in device memory outside
+ * its tensor (bit 1: a position, slot, page or length given to an attention
+ * entry; that access was skipped), or CONVROT_ERR_CUDA if the synchronisation
+ * itself failed.  If detail is not NULL it receives the raw error word (0 when
+ * clean).
  */
 convrot_status convrot_device_status(convrot_stream_t stream, uint32_t* detail);
 
@@ -341,6 +344,98 @@ convrot_status convrot_int8_gemm_s32(const int8_t* Xq, const int8_t* Wq, int M, 
 convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M, int N, int K,
                                      int32_t* acc, void* workspace, size_t workspace_bytes,
                                      convrot_stream_t stream);
+
+/* --------------------------------------------------------------------------
+ * Attention: what stands between the q/k/v projection and the o projection of
+ * the quantised decoder layer (the model cards quantise both and leave the
+ * attention itself to the runtime; no passage defines it, so the usual
+ * grouped-head softmax attention with half-split rotary positions is taken).
+ *
+ * Tensors of head rows are bf16 [rows, heads, D] with D = 64 or 128, heads
+ * and elements contiguous and `*_stride` elements from one row to the next (a
+ * multiple of 8, at least heads * D), so column views of a fused q/k/v output
+ * are taken as they are.  Query head h reads key/value head h / (q_heads /
+ * kv_heads); q_heads % kv_heads == 0, q_heads <= 1024.
+ *
+ * A paged cache is k_cache, v_cache [pages, kv_heads, page_size, D],
+ * contiguous, page_size a multiple of 16 up to 4096: bf16 (k_scale = v_scale =
+ * NULL), or int8 codes with fp32 scales [pages, kv_heads, page_size] (value =
+ * code * scale; scale = max|row| / 127 over the D elements of a token's head).
+ *
+ * Positions, slots, page numbers, lengths and offsets are read on the device.
+ * One outside its tensor is never followed: the token or row concerned is left
+ * out and convrot_device_status reports it (bit 1).
+ * ------------------------------------------------------------------------ */
+
+/*
+ * Rotates q and k by their positions and appends k and v to a paged cache.
+ *   x' = x, or with a norm weight x * (1 + w) / sqrt(mean x^2 + eps) per head
+ *   for i < rope_dim / 2, with c = rope[pos][i], s = rope[pos][rope_dim / 2 + i]:
+ *     (x'_i, x'_{i + rope_dim/2}) -> (x'_i c - x'_{i + rope_dim/2} s,
+ *                                     x'_{i + rope_dim/2} c + x'_i s)
+ *   elements from rope_dim on stay as they are; v is stored as it is.
+ * All in fp32, rounded once to bf16, or for an int8 cache to the row's codes
+ * (half to even).
+ * q [tokens, q_heads, D], k, v [tokens, kv_heads, D]  in
+ * rope       fp32 [rope_rows, rope_dim]  in   rope_dim % 16 == 0, 16 .. D
+ * positions  int32 [tokens]              in   rows of rope
+ * slots      int64 [tokens]              in   page * page_size + offset; a
+ *            negative one writes nothing to the cache (a padded token).  Two
+ *            tokens of a call must not have the same slot.
+ * q_norm, k_norm  fp32 [D] or NULL       in   16-byte aligned
+ * q_out      bf16 [tokens, q_heads, D]   out  may be q itself (same stride)
+ * k_out      bf16 [tokens, kv_heads, D] or NULL  out  rotated k; may be k itself
+ * k_cache, v_cache, k_scale, v_scale     in/out  only the slots' rows are written
+ */
+convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, int tokens, int q_heads,
+                                   int kv_heads, int head_dim, const float* rope, int rope_rows,
+                                   int rope_dim, const int32_t* positions, const int64_t* slots,
+                                   const float* q_norm, const float* k_norm, float eps, void* q_out,
+                                   int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                   void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                   int pages, int page_size, convrot_stream_t stream);
+
+/*
+ * Attention over whole prompts, packed one after another:
+ *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j
+ * over the keys j of the row's own sequence; causal != 0: row i of lq sees
+ * keys j <= i + lk - lq (the last row sees all).  A row that sees no key is 0.
+ * What a row does not see never reaches it, infinities and NaN included.
+ * q [tokens, q_heads, D]; k, v [kv_tokens, kv_heads, D]  in
+ * cu_q, cu_k int32 [seqs + 1]  in   non-decreasing offsets of the sequences'
+ *            first rows in q and in k, v (the same pointer when they agree)
+ * scale      > 0
+ * out        bf16 [tokens, q_heads, D]  out  rows of no sequence are left as
+ *            they were; out must not overlap an input
+ */
+convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                        const void* v, int64_t v_stride, int tokens, int kv_tokens,
+                                        int q_heads, int kv_heads, int head_dim, const int32_t* cu_q,
+                                        const int32_t* cu_k, int seqs, float scale, int causal, void* out,
+                                        int64_t out_stride, convrot_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over a paged cache (the new token's
+ * own key and value already appended):
+ *   o_b = sum_{j < lens[b]} softmax_j(scale * q_b . k_j) v_j;  0 when lens[b] = 0
+ * Key j of sequence b is row j % page_size of page table[b][j / page_size].
+ * q [seqs, q_heads, D]  in
+ * table      int32 [seqs, table_cols], rows table_stride apart  in  entries
+ *            past a sequence's last page are not read
+ * lens       int32 [seqs]  in   0 .. table_cols * page_size
+ * out        bf16 [seqs, q_heads, D]  out
+ * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte
+ *            aligned, zero-filled before its first use; every call leaves it
+ *            fit for the next.  Calls that overlap on the GPU need one each.
+ */
+size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim);
+convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seqs, int q_heads, int kv_heads,
+                                        int head_dim, const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale, int pages, int page_size,
+                                        const int32_t* table, int64_t table_stride, int table_cols,
+                                        const int32_t* lens, float scale, void* out, int64_t out_stride,
+                                        void* workspace, size_t workspace_bytes, convrot_stream_t stream);
 
 #ifdef __cplusplus
 }

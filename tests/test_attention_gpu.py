@@ -1,0 +1,550 @@
+"""The attention operators on the GPU against the float64 oracle: append with
+rotation, prompt attention and single-token attention over a paged cache.
+
+Tolerances are the oracle's bounds of the kernels' arithmetic
+(oracle/attention_ref.py): half a bf16 step per rounding plus the fp32 terms.
+Queries are drawn four times as wide as keys, so that a few keys carry most of
+a row's weight and a wrong key shows.
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import attention_ref as ref
+from tests import _tol
+
+pytestmark = pytest.mark.gpu
+
+U, BF16 = ref.U, ref.BF16
+TINY = 2.0 ** -134      # half a step of bfloat16's subnormals
+TINY32 = 2.0 ** -149    # a step of fp32's
+
+
+@pytest.fixture(scope="module")
+def cr():
+    if not torch.cuda.is_available():
+        pytest.skip("needs a CUDA device")
+    import w8a8_int8_quantized_rmsnorm_b200 as m
+    m.lib()
+    return m
+
+
+def f64(t):
+    return t.detach().float().cpu().double().numpy()
+
+
+def randn(seed, *shape, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g) * std).to(torch.bfloat16).cuda()
+
+
+def within(got, want, tol, what=""):
+    bad = ~(np.abs(got - want) <= tol)
+    assert not bad.any(), (f"{what}: {bad.sum()} of {bad.size} outside, first at {np.argwhere(bad)[0]}, worst "
+                           f"{np.max(np.abs(got - want) / np.maximum(tol, 1e-300))} times the bound")
+
+
+# ------------------------------------------------------------------ append
+def append_case(seed, T, Hq, Hkv, D, rot, page, i8, norm, pad=0, spare=2, rows=50):
+    fused = randn(seed, T, (Hq + 2 * Hkv) * D)
+    q, k, v = fused.split([Hq * D, Hkv * D, Hkv * D], 1)
+    pages = (T + page - 1) // page + spare
+    g = torch.Generator().manual_seed(seed + 1)
+    slots = torch.randperm(pages * page, generator=g)[:T]
+    if T:
+        slots[0] = pages * page - 1
+        slots = torch.where(torch.arange(T) >= T - pad, -1, slots)
+        slots[(slots == pages * page - 1) & (torch.arange(T) > 0)] = -1
+    shape = (pages, Hkv, page, D)
+    c = dict(q=q.view(T, Hq, D), k=k.view(T, Hkv, D), v=v.view(T, Hkv, D),
+             rope=torch.from_numpy(ref.rope_table(rows, rot)).cuda(),
+             positions=torch.randint(0, rows, (T,), generator=g, dtype=torch.int32).cuda(), slots=slots.cuda())
+    if i8:
+        c |= dict(k_cache=torch.randint(-127, 128, shape, generator=g, dtype=torch.int16).to(torch.int8).cuda(),
+                  v_cache=torch.randint(-127, 128, shape, generator=g, dtype=torch.int16).to(torch.int8).cuda(),
+                  k_scale=torch.rand(shape[:3], generator=g).cuda(), v_scale=torch.rand(shape[:3], generator=g).cuda())
+    else:
+        c |= dict(k_cache=randn(seed + 2, *shape), v_cache=randn(seed + 3, *shape))
+    if norm:
+        c |= dict(q_norm=torch.randn(D, generator=g).cuda() * 0.1, k_norm=torch.randn(D, generator=g).cuda() * 0.1)
+    return c
+
+
+def check_append(c, before, q_out, k_out, eps=1e-6):
+    rope, pos, slots = c["rope"].cpu().numpy(), c["positions"].cpu().numpy(), c["slots"].cpu().numpy()
+    w = {x: None if c.get(x) is None else f64(c[x]) for x in ("q_norm", "k_norm")}
+    q, qe = ref.norm_rotate(f64(before["q"]), w["q_norm"], rope, pos, eps)
+    k, ke = ref.norm_rotate(f64(before["k"]), w["k_norm"], rope, pos, eps)
+    v = f64(before["v"])
+    within(f64(q_out), q, BF16 * np.abs(q) + 2 * qe + TINY, "q")
+    if k_out is not None:
+        within(f64(k_out), k, BF16 * np.abs(k) + 2 * ke + TINY, "k")
+    page = c["k_cache"].shape[2]
+    live = slots >= 0
+    at = slots[live]
+    for name, y, err in (("k", k, ke), ("v", v, 0 * v)):
+        new, old = c[name + "_cache"].cpu(), before[name + "_cache"].cpu()
+        rows = f64(new)[at // page, :, at % page]
+        if c.get("k_scale") is None:
+            within(rows, y[live], BF16 * np.abs(y[live]) + 2 * err[live] + TINY, name + " cache")
+            if name == "v":
+                assert np.array_equal(rows, y[live])
+        else:
+            scale = c[name + "_scale"].cpu().double().numpy()[at // page, :, at % page]
+            y2, e2 = y[live].reshape(-1, y.shape[-1]), err[live].reshape(-1, y.shape[-1])
+            amax = np.abs(y2).max(1)
+            ratio = e2.max(1) / np.where(amax > 0, amax, 1)
+            s = amax / 127
+            assert np.all(np.abs(scale.reshape(-1) - s) <= s * _tol.scale_rel_tol(ratio, False) + TINY32), name + " scales"
+            z = y2 / np.where(s > 0, s, 1)[:, None]
+            _tol.check_codes(rows.reshape(z.shape), np.rint(z), z, _tol.int8_code_window(ratio), name)
+        # every other row of the cache is as it was
+        keep = np.ones(new.shape[0] * page, bool)
+        keep[at] = False
+        flat = [x.view(torch.uint8 if x.dtype == torch.int8 else torch.int16).transpose(1, 2).flatten(0, 1).numpy()
+                for x in (new, old)]
+        assert np.array_equal(flat[0][keep], flat[1][keep]), name + " cache: a row that is no slot changed"
+        if c.get("k_scale") is not None:
+            sc = [x.cpu().transpose(1, 2).flatten(0, 1).numpy() for x in (c[name + "_scale"], before[name + "_scale"])]
+            assert np.array_equal(sc[0][keep], sc[1][keep])
+
+
+def run_append(cr, c, k_out=True, **kw):
+    before = {n: t.clone() for n, t in c.items()}
+    ko = torch.empty(c["k"].shape, dtype=torch.bfloat16, device="cuda") if k_out is True else k_out
+    q, k = cr.convrot_rope_append(**c, k_out=ko, **kw)
+    torch.cuda.synchronize()
+    assert cr.convrot_device_status() == 0
+    return before, q, k
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("norm", [False, True])
+@pytest.mark.parametrize("T,Hq,Hkv,D,rot,page", [
+    (1, 32, 8, 128, 128, 16), (1, 1, 1, 64, 64, 16), (3, 5, 1, 64, 32, 48), (37, 8, 2, 128, 64, 16),
+    (130, 14, 2, 64, 16, 64), (300, 4, 4, 128, 128, 128), (33, 7, 7, 128, 16, 32), (1000, 32, 8, 128, 128, 64),
+    (9000, 2, 1, 64, 64, 4096)])
+def test_append(cr, T, Hq, Hkv, D, rot, page, norm, i8):
+    c = append_case(T + Hq, T, Hq, Hkv, D, rot, page, i8, norm, pad=T // 5)
+    before, q, k = run_append(cr, c)
+    check_append(c, before, q, k)
+
+
+def test_append_in_place_and_without_rotated_keys(cr):
+    c = append_case(5, 70, 8, 2, 128, 128, 16, False, True)
+    before = {n: t.clone() for n, t in c.items()}
+    q, k = cr.convrot_rope_append(**c, q_out=c["q"], k_out=c["k"])
+    assert q.data_ptr() == c["q"].data_ptr() and k.data_ptr() == c["k"].data_ptr()
+    check_append(c, before, q, k)
+    assert torch.equal(c["v"], before["v"])
+    c = append_case(6, 70, 8, 2, 128, 128, 16, True, False)
+    before, q, k = run_append(cr, c, k_out=None)
+    assert k is None
+    check_append(c, before, q, None)
+
+
+def test_append_one_norm_only(cr):
+    c = append_case(7, 21, 4, 2, 64, 64, 16, False, True)
+    c["q_norm"] = None
+    before = {n: None if t is None else t.clone() for n, t in c.items()}
+    ko = torch.empty_like(c["k"].contiguous())
+    q, k = cr.convrot_rope_append(**c, k_out=ko)
+    check_append(c, before, q, k)
+
+
+def test_append_extreme_rows_int8(cr):
+    """A zero row (scale 0), rows far below and far above one, and a row with a
+    NaN, whose scale says so."""
+    c = append_case(8, 6, 2, 1, 64, 64, 16, True, False)
+    k = c["k"].clone()
+    k[0] = 0
+    k[1] = k[1].float() * 2.0 ** -120
+    k[2] = k[2].float() * 2.0 ** 100
+    k[3] = k[3].float() * 1e-38
+    c["k"] = k
+    before, q, ko = run_append(cr, c)
+    check_append(c, before, q, ko)
+    c["k"][4, 0, 3] = float("nan")
+    run_append(cr, c)
+    page = c["k_cache"].shape[2]
+    at = int(c["slots"][4])
+    assert torch.isnan(c["k_scale"][at // page, 0, at % page])
+
+
+def test_append_unrotated_part_keeps_infinities(cr):
+    c = append_case(9, 3, 2, 1, 128, 64, 16, False, False)
+    c["k"] = c["k"].clone()
+    c["k"][1, 0, 100] = float("inf")
+    before, q, ko = run_append(cr, c)
+    assert torch.isinf(ko[1, 0, 100]) and torch.isfinite(ko).sum() == ko.numel() - 1
+
+
+def test_append_reports_indices_outside(cr):
+    """A position or slot outside its tensor: the token is left out, the others
+    are as ever, and the device status says so."""
+    for name, bad in (("positions", 50), ("positions", -1), ("slots", 10 ** 9)):
+        c = append_case(10, 40, 4, 2, 64, 64, 16, False, False)
+        c[name][7] = bad
+        before = {n: t.clone() for n, t in c.items()}
+        qo, ko = torch.zeros_like(c["q"].contiguous()), torch.zeros_like(c["k"].contiguous())
+        cr.convrot_rope_append(**c, q_out=qo, k_out=ko)
+        assert cr.convrot_device_status() == 2
+        assert cr.convrot_device_status() == 0
+        assert not qo[7].any() and not ko[7].any()
+        keep = torch.arange(40) != 7
+        c2 = {n: t[keep] if n in ("q", "k", "v", "positions", "slots") else t for n, t in c.items()}
+        b2 = {n: t[keep] if n in ("q", "k", "v", "positions", "slots") else t for n, t in before.items()}
+        check_append(c2, b2, qo[keep], ko[keep])
+
+
+# ------------------------------------------------------------------ prompt
+def prompt_case(seed, lens_q, lens_k, Hq, Hkv, D, spare=0):
+    cu_q, cu_k = (np.concatenate([[0], np.cumsum(x)]).astype(np.int32) for x in (lens_q, lens_k))
+    T, Tk = int(cu_q[-1]) + spare, int(cu_k[-1]) + spare
+    return (randn(seed, T, Hq, D, std=4.0), randn(seed + 1, Tk, Hkv, D), randn(seed + 2, Tk, Hkv, D), cu_q, cu_k)
+
+
+def check_prompt(cr, q, k, v, cu_q, cu_k, causal=True, scale=None, out=None):
+    got = cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu_q).cuda(), torch.from_numpy(cu_k).cuda(),
+                                      causal=causal, scale=scale, out=out)
+    torch.cuda.synchronize()
+    assert cr.convrot_device_status() == 0
+    o, tol = ref.packed_attention(f64(q), f64(k), f64(v), cu_q, cu_k, q.shape[2] ** -0.5 if scale is None else scale,
+                                  causal)
+    n = cu_q[-1]
+    within(f64(got)[:n], o[:n], tol[:n], "prompt")
+    return got
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,Hq,Hkv,D", [
+    ([1], 1, 1, 64), ([1], 32, 8, 128), ([2], 4, 1, 128), ([31], 8, 2, 64), ([64], 4, 1, 128), ([65], 4, 1, 128),
+    ([127], 2, 2, 128), ([128], 1, 1, 128), ([129], 3, 1, 128), ([255, 256, 257], 1, 1, 64), ([300], 5, 1, 128),
+    ([1, 1, 1, 1], 8, 8, 64), ([5, 0, 300, 64, 0], 8, 2, 128), ([0, 0], 2, 1, 64), ([511], 16, 2, 64),
+    ([40] * 9, 14, 2, 128), ([770], 6, 2, 128), ([90], 128, 1, 64), ([70], 200, 1, 128), ([1200, 3], 2, 1, 128)])
+def test_prompt(cr, lens, Hq, Hkv, D, causal):
+    check_prompt(cr, *prompt_case(sum(lens) + Hq, lens, lens, Hq, Hkv, D), causal=causal)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_with_keys_of_another_length(cr, D, causal):
+    """More keys than queries (a prompt's continuation), fewer (leading rows see
+    nothing and are zero), and none at all."""
+    lens_q, lens_k = [3, 130, 200, 17, 64, 1], [300, 257, 40, 0, 64, 129]
+    got = check_prompt(cr, *prompt_case(1, lens_q, lens_k, 4, 2, D), causal=causal)
+    assert not got[350:].view(torch.int16)[-82:-65].any()           # the sequence without keys
+    if causal:
+        assert not got[133:133 + 160].any()
+
+
+def test_prompt_strided_operands_and_untouched_rows(cr):
+    """q, k, v as column views of one fused buffer, out with rows further apart;
+    rows behind the last sequence stay as they were."""
+    T, Hq, Hkv, D = 400, 8, 2, 128
+    fused = randn(3, T, (Hq + 2 * Hkv) * D)
+    q, k, v = (x.view(T, -1, D) for x in fused.split([Hq * D, Hkv * D, Hkv * D], 1))
+    big = torch.full((T, Hq * D + 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = big[:, :Hq * D].view(T, Hq, D)
+    cu = np.array([0, 150, 333], np.int32)
+    check_prompt(cr, q, k, v, cu, cu, out=out)
+    assert (big[333:] == 7).all() and (big[:, Hq * D:] == 7).all()
+    first = np.array([20, 150, 333], np.int32)                      # rows before the first sequence, too
+    big.fill_(7.0)
+    got = cr.convrot_attention_prompt(q, k, v, torch.from_numpy(first).cuda(), out=out)
+    assert (big[:20] == 7).all() and not (got[20:333] == 7).all(-1).any()
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf"), 3.38e38])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 4, 1), (64, 2, 2)])
+def test_prompt_masked_places_do_not_leak(cr, bad, D, Hq, Hkv):
+    """Keys and values that a row does not see, of later positions, of other
+    sequences and of rows behind the last one, may be anything."""
+    lens = [200, 1, 150]
+    q, k, v, cu, _ = prompt_case(4, lens, lens, Hq, Hkv, D, spare=30)
+    k[180:201], v[180:201] = bad, bad      # seen by rows 180.. of the first sequence and by the second
+    k[351:], v[351:] = bad, bad
+    got = f64(cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda()))
+    o, tol = ref.packed_attention(f64(q)[:351], f64(k)[:351], f64(v)[:351], cu, cu, D ** -0.5, True)
+    ok = np.r_[0:180, 201:351]
+    within(got[ok], o[ok], tol[ok], "rows that do not see them")
+    if bad != bad:
+        assert np.isnan(got[180:201]).all()
+
+
+def test_prompt_scores_of_minus_infinity_and_large_scores(cr):
+    q, k, v, cu, _ = prompt_case(6, [160], [160], 2, 1, 128)
+    q[:, :, 0], k[:, :, 0] = 300.0, 0.0
+    k[5:40, :, 0] = -3e38                     # their scores are -inf: they take no part
+    k[100] = k[100].float() * 100             # scores of a thousand and more
+    got = f64(cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda()))
+    see = np.tril(np.ones((160, 160), bool))
+    see[:, 5:40] = False
+    o, tol = np.zeros(got.shape), np.zeros(got.shape)
+    for h in range(2):
+        o[:, h], tol[:, h] = ref.attention(f64(q)[:, h], f64(k)[:, 0], f64(v)[:, 0], 128 ** -0.5, see)
+    within(got, o, tol, "prompt")
+
+
+def test_prompt_scale_and_repeatability(cr):
+    q, k, v, cu, _ = prompt_case(8, [190, 77], [190, 77], 4, 2, 64)
+    a = check_prompt(cr, q, k, v, cu, cu, scale=0.01)
+    b = check_prompt(cr, q, k, v, cu, cu, scale=0.01)
+    assert torch.equal(a, b)
+    check_prompt(cr, q, k, v, cu, cu, scale=3.0)
+
+
+def test_prompt_reports_offsets_outside(cr):
+    q, k, v, cu, _ = prompt_case(9, [50, 60], [50, 60], 2, 1, 64)
+    good = check_prompt(cr, q, k, v, cu, cu)
+    out = torch.zeros_like(good)
+    cu_k = torch.tensor([0, 50, 111], dtype=torch.int32, device="cuda")   # one past the keys
+    cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda(), cu_k, out=out)
+    assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+    assert torch.equal(out[:50], good[:50]) and not out[50:].any()
+    cu_q = torch.tensor([0, 50, 200], dtype=torch.int32, device="cuda")
+    out.zero_()
+    cr.convrot_attention_prompt(q, k, v, cu_q, torch.from_numpy(cu).cuda(), out=out)
+    assert cr.convrot_device_status() == 2
+    assert torch.equal(out[:50], good[:50]) and not out[50:].any()
+
+
+def test_prompt_larger_packs_agree_with_single_prompts(cr):
+    """A row's result does not depend on what it is packed with."""
+    lens = [1, 700, 33, 1025, 256, 90]
+    q, k, v, cu, _ = prompt_case(10, lens, lens, 8, 2, 128)
+    whole = cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda())
+    for a, b in zip(cu, cu[1:]):
+        one = cr.convrot_attention_prompt(q[a:b], k[a:b], v[a:b], torch.tensor([0, b - a], dtype=torch.int32).cuda())
+        assert torch.equal(whole[a:b], one)
+
+
+# ------------------------------------------------------------------ decode
+def decode_case(seed, lens, Hq, Hkv, D, page, i8, fill=float("nan"), spare=2):
+    """A cache whose rows past every sequence's end hold `fill`."""
+    g = torch.Generator().manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pages, cols = sum(need) + spare, max(need + [1]) + 1
+    perm = torch.randperm(pages, generator=g)
+    table = torch.full((len(lens), cols), -7, dtype=torch.int32)
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    shape = (pages, Hkv, page, D)
+    live = torch.zeros(pages, page, dtype=torch.bool)
+    for i, n in enumerate(lens):
+        for j in range(need[i]):
+            live[table[i, j], :max(0, min(page, n - j * page))] = True
+    keep = live[:, None, :].expand(shape[:3])
+    c = dict(q=randn(seed + 1, len(lens), Hq, D, std=4.0))
+    if i8:
+        for x in "kv":
+            codes = torch.randint(-127, 128, shape, generator=g, dtype=torch.int16).to(torch.int8)
+            scale = torch.rand(shape[:3], generator=g) * 0.02 + 0.005
+            scale[~keep] = fill
+            c |= {x + "_cache": codes.cuda(), x + "_scale": scale.cuda()}
+    else:
+        for i, x in enumerate("kv"):
+            t = torch.randn(shape, generator=g).to(torch.bfloat16)
+            t[~keep] = fill
+            c[x + "_cache"] = t.cuda()
+    return c | dict(block_table=table.cuda(), seq_lens=torch.tensor(lens, dtype=torch.int32).cuda())
+
+
+def oracle_decode(c, lens, scale=None):
+    s = [None if c.get(x) is None else c[x].cpu().double().numpy() for x in ("k_scale", "v_scale")]
+    return ref.paged_attention(f64(c["q"]), f64(c["k_cache"]), f64(c["v_cache"]), *s, c["block_table"].cpu().numpy(),
+                               lens, c["q"].shape[2] ** -0.5 if scale is None else scale)
+
+
+def check_decode(cr, c, lens, **kw):
+    got = cr.convrot_attention_decode(**c, **kw)
+    torch.cuda.synchronize()
+    assert cr.convrot_device_status() == 0
+    o, tol = oracle_decode(c, lens, kw.get("scale"))
+    within(f64(got), o, tol, "decode")
+    return got
+
+
+LENS = [[1], [0], [15, 16, 17, 0, 1], [63, 64, 65, 127, 128, 129], [1000], [5, 3000, 0, 70, 1, 250]]
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page", [(32, 8, 128, 16), (4, 4, 64, 64), (5, 1, 128, 48), (16, 2, 64, 32),
+                                           (9, 1, 64, 128), (20, 1, 128, 16), (14, 2, 128, 1024), (6, 3, 64, 16)])
+@pytest.mark.parametrize("lens", LENS, ids=[str(x)[:20] for x in LENS])
+def test_decode(cr, lens, Hq, Hkv, D, page, i8):
+    """Rows past a sequence's end, unused pages and unused table entries hold
+    NaN or nonsense and must not matter."""
+    check_decode(cr, decode_case(sum(lens) + Hq, lens, Hq, Hkv, D, page, i8), lens)
+
+
+@pytest.mark.parametrize("i8", [False, True])
+def test_decode_long_and_many(cr, i8):
+    check_decode(cr, decode_case(1, [20011], 4, 1, 128, 64, i8), [20011])
+    lens = [(i * 37) % 190 for i in range(333)]
+    check_decode(cr, decode_case(2, lens, 4, 2, 64, 16, i8, fill=float("inf")), lens)
+
+
+def test_decode_strided_operands(cr):
+    lens = [70, 5, 130]
+    c = decode_case(3, lens, 8, 2, 128, 16, False)
+    fused = torch.zeros(3, 12 * 128, dtype=torch.bfloat16, device="cuda")
+    fused[:, :1024] = c["q"].flatten(1)
+    c["q"] = fused[:, :1024].view(3, 8, 128)
+    wide = torch.full((3, 40), -9, dtype=torch.int32, device="cuda")
+    wide[:, :c["block_table"].shape[1]] = c["block_table"]
+    c["block_table"] = wide[:, :c["block_table"].shape[1]]
+    big = torch.full((3, 8 * 128 + 8), 7.0, dtype=torch.bfloat16, device="cuda")
+    check_decode(cr, c, lens, out=big[:, :1024].view(3, 8, 128), scale=0.05)
+    assert (big[:, 1024:] == 7).all()
+
+
+def test_decode_infinite_scores(cr):
+    lens = [90]
+    c = decode_case(4, lens, 2, 1, 64, 16, False, fill=0.0)
+    c["q"][..., 0] = 300.0
+    c["k_cache"][..., 0] = 0.0
+    first = int(c["block_table"][0, 0])
+    c["k_cache"][first, 0, 3:9, 0] = -3e38                  # scores of -inf
+    got = f64(cr.convrot_attention_decode(**c))
+    c2 = dict(c, k_cache=c["k_cache"].clone())
+    rows = np.ones((1, 90), bool)
+    rows[0, 3:9] = False
+    k = ref.cache_rows(f64(c2["k_cache"]), None, c["block_table"].cpu().numpy()[0], 90)[:, 0]
+    v = ref.cache_rows(f64(c["v_cache"]), None, c["block_table"].cpu().numpy()[0], 90)[:, 0]
+    k[3:9, 0] = 0
+    for h in range(2):
+        o, tol = ref.attention(f64(c["q"])[0, h][None], k, v, 64 ** -0.5, rows)
+        within(got[0, h], o[0], tol[0], "decode")
+
+
+def test_decode_reports_pages_and_lengths_outside(cr):
+    lens = [70, 40, 33]
+    c = decode_case(5, lens, 4, 2, 64, 16, False)
+    good = check_decode(cr, c, lens)
+    for bad in (-1, 10 ** 6):
+        d = dict(c, block_table=c["block_table"].clone())
+        d["block_table"][1, 1] = bad
+        got = cr.convrot_attention_decode(**d)
+        assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+        assert torch.equal(got[[0, 2]], good[[0, 2]]) and torch.isfinite(got).all()
+    for bad in (-3, 10 ** 6):
+        d = dict(c, seq_lens=c["seq_lens"].clone())
+        d["seq_lens"][0] = bad
+        got = cr.convrot_attention_decode(**d)
+        assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+        assert torch.equal(got[1:], good[1:]) and not got[0].any()
+
+
+def test_decode_is_repeatable_and_batch_independent_in_value(cr):
+    lens = [3000, 1, 700, 64]
+    c = decode_case(6, lens, 8, 2, 128, 32, False)
+    a = check_decode(cr, c, lens)
+    for _ in range(3):
+        assert torch.equal(a, cr.convrot_attention_decode(**c))
+
+
+@pytest.mark.parametrize("i8", [False, True])
+def test_cache_offsets_past_32_bits(cr, i8):
+    """Pages whose rows start past 2^31 elements (and past 2^32 bytes)."""
+    Hkv, page, D, lens = 8, 64, 128, [100, 64]
+    pages = (1 << 31) // (Hkv * page * D) + 6
+    shape = (pages, Hkv, page, D)
+    dt = torch.int8 if i8 else torch.bfloat16
+    c = dict(k_cache=torch.zeros(shape, dtype=dt, device="cuda"), v_cache=torch.zeros(shape, dtype=dt, device="cuda"))
+    if i8:
+        c |= dict(k_scale=torch.zeros(shape[:3], device="cuda"), v_scale=torch.zeros(shape[:3], device="cuda"))
+    table = torch.tensor([[pages - 1, pages - 3], [pages - 4, 0]], dtype=torch.int32)
+    T, Hq = sum(lens), 16
+    q, k, v = randn(1, T, Hq, D, std=4.0), randn(2, T, Hkv, D), randn(3, T, Hkv, D)
+    run = np.concatenate([np.arange(n) for n in lens])
+    seq = np.repeat([0, 1], lens)
+    slots = torch.from_numpy(table.numpy()[seq, run // page].astype(np.int64) * page + run % page)
+    rope = torch.from_numpy(ref.rope_table(200, D)).cuda()
+    ko = torch.empty_like(k)
+    cr.convrot_rope_append(q, k, v, rope, torch.from_numpy(run.astype(np.int32)).cuda(), slots.cuda(), **c, k_out=ko)
+    mine = {x: t[pages - 4:].clone() for x, t in c.items()}
+    assert not any(t[:pages - 4].any() for t in c.values())
+    small = table - (pages - 4)
+    got = cr.convrot_attention_decode(q[:2], block_table=table.cuda(), seq_lens=torch.tensor(lens, dtype=torch.int32).cuda(), **c)
+    near = dict(mine, q=q[:2], block_table=small.clamp_min(0), seq_lens=None)
+    o, tol = oracle_decode(near, lens)
+    assert cr.convrot_device_status() == 0
+    within(f64(got), o, tol, "decode")
+    if not i8:
+        page_of = small.numpy()[seq, run // page]
+        assert torch.equal(mine["v_cache"].cpu()[page_of, :, run % page], v.cpu())
+        assert torch.equal(mine["k_cache"].cpu()[page_of, :, run % page], ko.cpu())
+
+
+# ------------------------------------------------------------------ streams and graphs
+def test_other_streams_at_the_same_time(cr):
+    """Calls on two streams at once, each with results of its own."""
+    cases = [decode_case(20 + i, [2500, 31], 8, 2, 128, 16, bool(i)) for i in range(2)]
+    want = [cr.convrot_attention_decode(**c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(cr.convrot_attention_decode(**cases[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            assert torch.equal(g, want[i])
+
+
+def test_two_captured_graphs_replayed_at_the_same_time(cr):
+    """Graphs captured one after another on the same stream and replayed on two
+    others share no scratch memory; replays see new inputs and lengths."""
+    cases = [decode_case(30 + i, [2600, 31, 900], 8, 2, 128, 16, bool(i)) for i in range(2)]
+    outs, graphs = [], []
+    for c in cases:
+        cr.convrot_attention_decode(**c)
+    torch.cuda.synchronize()
+    for c in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(cr.convrot_attention_decode(**c))
+        graphs.append(g)
+    for new in ([2600, 31, 900], [1, 0, 333]):
+        for c in cases:
+            c["seq_lens"].copy_(torch.tensor(new, dtype=torch.int32))
+            c["q"].copy_(c["q"].flip(0))
+        want = [cr.convrot_attention_decode(**c) for c in cases]
+        torch.cuda.synchronize()
+        streams = [torch.cuda.Stream() for _ in cases]
+        for _ in range(20):
+            for g, s in zip(graphs, streams):
+                with torch.cuda.stream(s):
+                    g.replay()
+        torch.cuda.synchronize()
+        for o, w in zip(outs, want):
+            assert torch.equal(o, w)
+    assert cr.convrot_device_status() == 0
+
+
+def test_captured_append_and_prompt(cr):
+    c = append_case(40, 64, 8, 2, 128, 128, 16, False, True)
+    q, k, v, cu, _ = prompt_case(41, [60, 200], [60, 200], 4, 2, 64)
+    cu = torch.from_numpy(cu).cuda()
+    ko = torch.empty(c["k"].shape, dtype=torch.bfloat16, device="cuda")
+    cr.convrot_rope_append(**c, k_out=ko), cr.convrot_attention_prompt(q, k, v, cu)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        qo, _ = cr.convrot_rope_append(**c, k_out=ko)
+        o = cr.convrot_attention_prompt(q, k, v, cu)
+    c["q"].copy_(c["q"].flip(0))
+    c["slots"].copy_(c["slots"].flip(0))
+    q.copy_(q.flip(0))
+    cu.copy_(torch.tensor([0, 130, 260]))
+    before = {n: t.clone() for n, t in c.items()}
+    g.replay()
+    torch.cuda.synchronize()
+    check_append(c, before, qo, ko)
+    ref_o, tol = ref.packed_attention(f64(q), f64(k), f64(v), [0, 130, 260], [0, 130, 260], 64 ** -0.5, True)
+    within(f64(o), ref_o, tol, "replayed prompt")

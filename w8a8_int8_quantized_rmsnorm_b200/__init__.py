@@ -24,6 +24,8 @@ __all__ = [
     "convrot_interleave_gate_up", "convrot_fold_row_scales",
     "convrot_rotate_act_bf16", "convrot_weight_only_workspace_bytes", "convrot_weight_only_linear",
     "convrot_weight_only_gemm_f32",
+    "convrot_rope_append", "convrot_attention_prompt",
+    "convrot_attention_decode_workspace_bytes", "convrot_attention_decode",
     "Workspace", "ConvRotLinear", "ConvRotFusedLinear", "ConvRotMLP",
 ]
 
@@ -105,12 +107,13 @@ def _note_status(st: int) -> None:
 def convrot_device_status(device=None) -> int:
     """Synchronises the current stream and returns/clears the device error word.
 
-    A non-zero word means a kernel gave up on a bounded wait; every Workspace
-    is then zero-filled again before its next use."""
+    Bit 0: a kernel gave up on a bounded wait; every Workspace is then
+    zero-filled again before its next use.  Bit 1: an attention kernel met a
+    position, slot, page or length outside its tensor and left that access out."""
     dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
     detail = ctypes.c_uint32(0)
     st = lib().convrot_device_status(_stream(dev), ctypes.byref(detail))
-    if st not in (0, 6):
+    if st not in (0, 2, 6):
         _check("convrot_device_status", st)
     _note_status(st)
     return int(detail.value)
@@ -415,6 +418,143 @@ def convrot_fold_row_scales(s_row: torch.Tensor, smooth: torch.Tensor) -> torch.
     _check("convrot_fold_row_scales", lib().convrot_fold_row_scales(
         _ptr(s_row), _ptr(smooth), s_row.numel(), _stream(s_row.device)))
     return s_row
+
+
+# ---------------------------------------------------------------- attention
+def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, heads: Optional[int] = None,
+           dim: Optional[int] = None):
+    """A bf16 [rows, heads, D] operand whose heads lie next to one another; rows
+    may be further apart (a column view of a fused projection's output)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dimensions [rows, heads, D]")
+    r, h, d = t.shape
+    for got, want, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "elements per head")):
+        if want is not None and got != want:
+            raise ValueError(f"{name} must have {want} {what}, got {got}")
+    sr, sh, sd = t.stride()
+    if t.numel() and (sd != 1 or (h > 1 and sh != d) or (r > 1 and (sr < h * d or sr % 8))):
+        raise ValueError(f"{name} must have contiguous heads and rows a multiple of 8 elements apart, got strides {t.stride()}")
+    return r, h, d
+
+
+def _row_stride(t: torch.Tensor) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+
+
+def _cache(k_cache, v_cache, k_scale, v_scale):
+    """Checks a paged cache; returns (pages, kv_heads, page_size, D)."""
+    i8 = k_scale is not None or v_scale is not None
+    dtype = torch.int8 if i8 else torch.bfloat16
+    _need(k_cache, dtype, "k_cache", 4)
+    _need(v_cache, dtype, "v_cache", shape=k_cache.shape)
+    if i8:
+        _need(k_scale, torch.float32, "k_scale", shape=k_cache.shape[:3])
+        _need(v_scale, torch.float32, "v_scale", shape=k_cache.shape[:3])
+    return k_cache.shape
+
+
+def convrot_rope_append(q, k, v, rope, positions, slots, k_cache, v_cache, *, k_scale=None, v_scale=None,
+                        q_norm=None, k_norm=None, eps: float = 1e-6, q_out=None, k_out=None):
+    """Rotates q and k (after an optional per-head RMSNorm) by their positions'
+    rows of the table `rope` and writes k and v into a paged cache at `slots`
+    (page * page_size + offset; negative: nowhere).  Returns (q_out, k_out);
+    the rotated k is written only where the caller gives a k_out.  q_out and
+    k_out may be q and k themselves."""
+    T, Hq, D = _heads(q, "q")
+    Hkv = _heads(k, "k", T, None, D)[1]
+    _heads(v, "v", T, Hkv, D)
+    pages, _, page_size, _ = _cache(k_cache, v_cache, k_scale, v_scale)
+    if k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+        raise ValueError(f"k_cache must hold {Hkv} heads of {D} elements, got shape {tuple(k_cache.shape)}")
+    _need(rope, torch.float32, "rope", 2)
+    _need(positions, torch.int32, "positions", shape=(T,))
+    _need(slots, torch.int64, "slots", shape=(T,))
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _need(w, torch.float32, name, shape=(D,))
+    if q_out is not None:
+        _heads(q_out, "q_out", T, Hq, D)
+    if k_out is not None:
+        _heads(k_out, "k_out", T, Hkv, D)
+    dev = _on_device(q=q, k=k, v=v, rope=rope, positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache,
+                     k_scale=k_scale, v_scale=v_scale, q_norm=q_norm, k_norm=k_norm, q_out=q_out, k_out=k_out)
+    if q_out is None:
+        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    _check("convrot_rope_append", lib().convrot_rope_append(
+        _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), T, Hq, Hkv, D, _ptr(rope),
+        rope.shape[0], rope.shape[1], _ptr(positions), _ptr(slots), _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out),
+        _row_stride(q_out), _ptr(k_out), 0 if k_out is None else _row_stride(k_out), _ptr(k_cache), _ptr(v_cache),
+        _ptr(k_scale), _ptr(v_scale), pages, page_size, _stream(dev)))
+    return q_out, k_out
+
+
+def convrot_attention_prompt(q, k, v, cu_seqlens, cu_seqlens_k=None, *, scale: Optional[float] = None,
+                             causal: bool = True, out=None):
+    """Attention over whole prompts packed one after another: sequence i is rows
+    cu_seqlens[i] .. cu_seqlens[i + 1] of q, and of k and v unless they have
+    offsets of their own.  scale None: D ** -0.5.  A new `out` is not
+    initialised: rows of no sequence hold what the memory held."""
+    T, Hq, D = _heads(q, "q")
+    Tk, Hkv, _ = _heads(k, "k", None, None, D)
+    _heads(v, "v", Tk, Hkv, D)
+    _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    if cu_seqlens_k is None:
+        if Tk != T:
+            raise ValueError("k and q have different lengths: cu_seqlens_k is needed")
+        cu_seqlens_k = cu_seqlens
+    else:
+        _need(cu_seqlens_k, torch.int32, "cu_seqlens_k", shape=cu_seqlens.shape)
+    if cu_seqlens.numel() < 1:
+        raise ValueError("cu_seqlens must hold one offset more than there are sequences")
+    if out is not None:
+        _heads(out, "out", T, Hq, D)
+    dev = _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, out=out)
+    if out is None:
+        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+    _check("convrot_attention_prompt", lib().convrot_attention_prompt(
+        _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), T, Tk, Hq, Hkv, D, _ptr(cu_seqlens),
+        _ptr(cu_seqlens_k), cu_seqlens.numel() - 1, D ** -0.5 if scale is None else scale, int(causal), _ptr(out),
+        _row_stride(out), _stream(dev)))
+    return out
+
+
+def convrot_attention_decode_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(lib().convrot_attention_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim))
+
+
+def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None,
+                             scale: Optional[float] = None, out=None, workspace: Optional[Workspace] = None):
+    """Attention of one new token per sequence over a paged cache (bf16, or
+    int8 with scales).  seq_lens counts the new token, whose key and value the
+    cache already holds.  scale None: D ** -0.5."""
+    B, Hq, D = _heads(q, "q")
+    pages, Hkv, page_size, Dc = _cache(k_cache, v_cache, k_scale, v_scale)
+    if Dc != D:
+        raise ValueError(f"q has {D} elements per head, the cache {Dc}")
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+        raise TypeError("block_table must be a torch.int32 tensor")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError(f"block_table must have shape ({B}, pages per sequence), got {tuple(block_table.shape)}")
+    cols = block_table.shape[1]
+    if block_table.numel() and ((cols > 1 and block_table.stride(1) != 1) or (B > 1 and block_table.stride(0) < cols)):
+        raise ValueError("block_table must have contiguous rows")
+    _need(seq_lens, torch.int32, "seq_lens", shape=(B,))
+    if out is not None:
+        _heads(out, "out", B, Hq, D)
+    dev = _on_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
+                     k_scale=k_scale, v_scale=v_scale, out=out)
+    if out is None:
+        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
+    ws, wn = _workspace(dev, convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D), workspace)
+    _check("convrot_attention_decode", lib().convrot_attention_decode(
+        _ptr(q), _row_stride(q), B, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages,
+        page_size, _ptr(block_table), max(cols, block_table.stride(0)) if B > 1 else cols, cols, _ptr(seq_lens),
+        D ** -0.5 if scale is None else scale, _ptr(out), _row_stride(out), ws, wn, _stream(dev)))
+    return out
 
 
 class ConvRotLinear:

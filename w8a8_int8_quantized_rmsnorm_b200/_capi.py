@@ -12,6 +12,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libconvrot.so")
 
 c_int = ctypes.c_int
+c_int64 = ctypes.c_int64
 c_float = ctypes.c_float
 c_size_t = ctypes.c_size_t
 c_void_p = ctypes.c_void_p
@@ -65,6 +66,15 @@ SIGNATURES = {
                                              c_void_p, c_size_t, c_void_p]),
     "convrot_int8_linear_noalloc": (c_int, [c_void_p, c_void_p, c_void_p, c_void_p, c_int, c_int,
                                             c_int, c_void_p, c_void_p]),
+    "convrot_rope_append": (c_int, [c_void_p, c_int64] * 3 + [c_int] * 4 + [c_void_p, c_int, c_int]
+                            + [c_void_p] * 4 + [c_float] + [c_void_p, c_int64] * 2 + [c_void_p] * 4
+                            + [c_int, c_int, c_void_p]),
+    "convrot_attention_prompt": (c_int, [c_void_p, c_int64] * 3 + [c_int] * 5 + [c_void_p, c_void_p, c_int, c_float,
+                                         c_int, c_void_p, c_int64, c_void_p]),
+    "convrot_attention_decode_workspace_bytes": (c_size_t, [c_int] * 4),
+    "convrot_attention_decode": (c_int, [c_void_p, c_int64] + [c_int] * 4 + [c_void_p] * 4 + [c_int, c_int, c_void_p,
+                                         c_int64, c_int, c_void_p, c_float, c_void_p, c_int64, c_void_p, c_size_t,
+                                         c_void_p]),
     "convrot_int8_gemm_s32": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p,
                                       c_void_p, c_size_t, c_void_p]),
     "convrot_w4a8_gemm_s32": (c_int, [c_void_p, c_void_p, c_int, c_int, c_int, c_void_p,

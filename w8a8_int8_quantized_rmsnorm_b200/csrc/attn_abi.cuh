@@ -1,0 +1,194 @@
+// Host side of the attention entry points: validation and launches.
+// Included by convrot_abi.cu, whose helpers it uses.
+#pragma once
+
+#include "append.cuh"
+#include "attn_decode.cuh"
+#include "attn_prompt.cuh"
+
+namespace {
+
+constexpr int kMaxHeads = 1024;
+constexpr int kMaxPage = 4096;
+
+// Heads, head size and a row stride (elements) of a [rows, heads, D] tensor.
+bool heads_ok(int q_heads, int kv_heads) {
+  return q_heads > 0 && kv_heads > 0 && q_heads <= kMaxHeads && q_heads % kv_heads == 0;
+}
+bool stride_ok(int64_t stride, int heads, int D, int rows) {
+  return stride % 8 == 0 && (rows <= 1 || stride >= static_cast<int64_t>(heads) * D);
+}
+
+convrot_status run_append(const AppendArgs& args, int D, bool int8, cudaStream_t st) {
+  const DeviceInfo d = current_device();
+  if (d.device < 0 || d.sms <= 0) return CONVROT_ERR_CUDA;
+  AppendArgs a = args;
+  const int lanes = D / 16, groups = ((a.q_heads + 2 * a.kv_heads) * lanes + 31) / 32;
+  // warps per token: one where the tokens alone fill the GPU, else up to one
+  // per row group (a single token's rows then load side by side)
+  const int64_t want = static_cast<int64_t>(d.sms) * 32;
+  a.parts = static_cast<int>(std::min<int64_t>(groups, std::max<int64_t>(1, want / a.tokens)));
+  const int64_t warps = static_cast<int64_t>(a.tokens) * a.parts;
+  const unsigned blocks = static_cast<unsigned>((warps + APPEND_WARPS - 1) / APPEND_WARPS);
+  auto k = D == 128 ? (int8 ? append_kernel<128, true> : append_kernel<128, false>)
+                    : (int8 ? append_kernel<64, true> : append_kernel<64, false>);
+  return launch_pdl(k, dim3(blocks), dim3(32 * APPEND_WARPS), 0, st, 1, a);
+}
+
+}  // namespace
+
+extern "C" {
+
+convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                   const void* v, int64_t v_stride, int tokens, int q_heads,
+                                   int kv_heads, int head_dim, const float* rope, int rope_rows,
+                                   int rope_dim, const int32_t* positions, const int64_t* slots,
+                                   const float* q_norm, const float* k_norm, float eps, void* q_out,
+                                   int64_t q_out_stride, void* k_out, int64_t k_out_stride,
+                                   void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                                   int pages, int page_size, convrot_stream_t stream) {
+  if (tokens < 0 || !heads_ok(q_heads, kv_heads)) return CONVROT_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return CONVROT_ERR_UNSUPPORTED;
+  if (tokens > (1 << 24) || pages < 0 || page_size < 1 || page_size > kMaxPage || page_size % 16)
+    return CONVROT_ERR_SHAPE;
+  if (rope_rows < 1 || rope_dim < 16 || rope_dim > head_dim || rope_dim % 16) return CONVROT_ERR_SHAPE;
+  if ((q_norm || k_norm) && !(eps >= 0.f)) return CONVROT_ERR_SHAPE;
+  if (!stride_ok(q_stride, q_heads, head_dim, tokens) || !stride_ok(k_stride, kv_heads, head_dim, tokens) ||
+      !stride_ok(v_stride, kv_heads, head_dim, tokens) ||
+      !stride_ok(q_out_stride, q_heads, head_dim, tokens) ||
+      (k_out && !stride_ok(k_out_stride, kv_heads, head_dim, tokens)))
+    return CONVROT_ERR_SHAPE;
+  if (tokens == 0) return CONVROT_OK;
+  if (!q || !k || !v || !rope || !positions || !slots || !q_out || !k_cache || !v_cache || !k_scale != !v_scale)
+    return CONVROT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(rope, 16) || !aligned(positions, 4) ||
+      !aligned(slots, 8) || !aligned(q_out, 16) || !aligned(k_out, 16) || !aligned(k_cache, 16) ||
+      !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(q_norm, 16) ||
+      !aligned(k_norm, 16))
+    return CONVROT_ERR_ALIGN;
+  AppendArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.rope = rope;
+  a.positions = positions;
+  a.slots = slots;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.k_out = static_cast<uint16_t*>(k_out);
+  a.q_out_stride = q_out_stride;
+  a.k_out_stride = k_out_stride;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.slot_end = static_cast<int64_t>(pages) * page_size;
+  a.tokens = tokens;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.rope_rows = rope_rows;
+  a.rope_dim = rope_dim;
+  a.page_size = page_size;
+  a.eps = eps;
+  return run_append(a, head_dim, k_scale != nullptr, as_cuda(stream));
+}
+
+convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                        const void* v, int64_t v_stride, int tokens, int kv_tokens,
+                                        int q_heads, int kv_heads, int head_dim, const int32_t* cu_q,
+                                        const int32_t* cu_k, int seqs, float scale, int causal, void* out,
+                                        int64_t out_stride, convrot_stream_t stream) {
+  if (tokens < 0 || kv_tokens < 0 || seqs < 0 || !heads_ok(q_heads, kv_heads)) return CONVROT_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return CONVROT_ERR_UNSUPPORTED;
+  if (tokens > (1 << 24) || kv_tokens > (1 << 24) || seqs > (1 << 24)) return CONVROT_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return CONVROT_ERR_SHAPE;
+  if (!stride_ok(q_stride, q_heads, head_dim, tokens) || !stride_ok(k_stride, kv_heads, head_dim, kv_tokens) ||
+      !stride_ok(v_stride, kv_heads, head_dim, kv_tokens) || !stride_ok(out_stride, q_heads, head_dim, tokens))
+    return CONVROT_ERR_SHAPE;
+  if (tokens == 0 || seqs == 0) return CONVROT_OK;
+  if (!q || !out || !cu_q || !cu_k || (kv_tokens > 0 && (!k || !v))) return CONVROT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
+      !aligned(cu_k, 4))
+    return CONVROT_ERR_ALIGN;
+  PromptArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.k = static_cast<const uint16_t*>(k);
+  a.v = static_cast<const uint16_t*>(v);
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.o_stride = out_stride;
+  a.o = static_cast<uint16_t*>(out);
+  a.cu_q = cu_q;
+  a.cu_k = cu_k;
+  a.tokens = tokens;
+  a.kv_tokens = kv_tokens;
+  a.seqs = seqs;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.scale_log2 = scale * LOG2E;
+  a.causal = causal != 0;
+  const int64_t warps = static_cast<int64_t>(tokens) * q_heads;
+  return launch_pdl(head_dim == 128 ? prompt_rows_kernel<128> : prompt_rows_kernel<64>,
+                    dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, as_cuda(stream), 1, a);
+}
+
+size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
+  (void)seqs;
+  if (!heads_ok(q_heads, kv_heads) || (head_dim != 64 && head_dim != 128)) return 0;
+  return 0;
+}
+
+convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seqs, int q_heads, int kv_heads,
+                                        int head_dim, const void* k_cache, const void* v_cache,
+                                        const float* k_scale, const float* v_scale, int pages, int page_size,
+                                        const int32_t* table, int64_t table_stride, int table_cols,
+                                        const int32_t* lens, float scale, void* out, int64_t out_stride,
+                                        void* workspace, size_t workspace_bytes, convrot_stream_t stream) {
+  (void)workspace;
+  (void)workspace_bytes;
+  if (seqs < 0 || !heads_ok(q_heads, kv_heads)) return CONVROT_ERR_SHAPE;
+  if (head_dim != 64 && head_dim != 128) return CONVROT_ERR_UNSUPPORTED;
+  if (seqs > (1 << 24) || pages < 0 || page_size < 1 || page_size > kMaxPage || page_size % 16 || table_cols < 0)
+    return CONVROT_ERR_SHAPE;
+  if (seqs > 1 && table_stride < table_cols) return CONVROT_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale < INFINITY)) return CONVROT_ERR_SHAPE;
+  if (!stride_ok(q_stride, q_heads, head_dim, seqs) || !stride_ok(out_stride, q_heads, head_dim, seqs))
+    return CONVROT_ERR_SHAPE;
+  if (seqs == 0) return CONVROT_OK;
+  if (!q || !out || !lens || !k_scale != !v_scale) return CONVROT_ERR_NULL;
+  if ((pages > 0 && (!k_cache || !v_cache)) || (table_cols > 0 && !table)) return CONVROT_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(table, 4) || !aligned(lens, 4))
+    return CONVROT_ERR_ALIGN;
+  DecodeArgs a{};
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_stride = q_stride;
+  a.o_stride = out_stride;
+  a.o = static_cast<uint16_t*>(out);
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = table;
+  a.table_stride = table_stride;
+  a.lens = lens;
+  a.seqs = seqs;
+  a.q_heads = q_heads;
+  a.kv_heads = kv_heads;
+  a.pages = pages;
+  a.page_size = page_size;
+  a.table_cols = table_cols;
+  a.scale_log2 = scale * LOG2E;
+  const int64_t warps = static_cast<int64_t>(seqs) * q_heads;
+  const bool i8 = k_scale != nullptr;
+  auto kern = head_dim == 128 ? (i8 ? decode_rows_kernel<128, true> : decode_rows_kernel<128, false>)
+                              : (i8 ? decode_rows_kernel<64, true> : decode_rows_kernel<64, false>);
+  return launch_pdl(kern, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, as_cuda(stream), 1, a);
+}
+
+}  // extern "C"

@@ -2,7 +2,8 @@
 //
 // Host side only: argument validation, TMA tensor-map encoding, launch
 // configuration and the work schedule of the GEMM.  All arithmetic of the
-// method runs in the kernels of rowquant.cuh and gemm.cuh.
+// method runs in the kernels of rowquant.cuh and gemm.cuh.  The attention
+// entry points are in attn_abi.cuh, included at the end.
 #include <cuda.h>
 #include <cuda_runtime.h>
 
@@ -854,6 +855,8 @@ convrot_status convrot_device_status(convrot_stream_t stream, uint32_t* detail) 
   if (v && cudaMemcpyToSymbol(g_error_word, &zero, sizeof(zero)) != cudaSuccess)
     return CONVROT_ERR_CUDA;
   if (detail) *detail = v;
+  // only bad indices (bit 1): every kernel completed, no workspace is in doubt
+  if (v == ERR_BAD_ARGUMENT) return CONVROT_ERR_SHAPE;
   if (v) g_timeouts_reported.fetch_add(1u, std::memory_order_relaxed);
   return v ? CONVROT_ERR_DEVICE_TIMEOUT : CONVROT_OK;
 }
@@ -1255,3 +1258,6 @@ extern "C" convrot_status convrot_int8_linear_noalloc(const int8_t* Xq, const fl
   return run_gemm(Xq, Wq, false, s_tok, s_row, M, N, K, Y, EPI_BF16, ws,
                   need > 0 ? kStaticWorkspaceBytes : 0, as_cuda(stream));
 }
+
+// The attention entry points.
+#include "attn_abi.cuh"

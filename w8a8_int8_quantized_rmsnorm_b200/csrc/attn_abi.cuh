@@ -35,6 +35,52 @@ convrot_status run_append(const AppendArgs& args, int D, bool int8, cudaStream_t
   return launch_pdl(k, dim3(blocks), dim3(32 * APPEND_WARPS), 0, st, 1, a);
 }
 
+// bf16 head rows as a 3-D map (element, head, row) with boxes of 64 elements,
+// `box_heads` heads and `box_rows` rows, 128-byte swizzle.
+bool make_heads_map(CUtensorMap* map, const void* base, int rows, int heads, int D, int64_t stride, int box_heads,
+                    int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(heads), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, static_cast<cuuint64_t>(stride) * 2};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_heads), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D>
+convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
+  PromptArgs a = args;
+  const DeviceInfo d = current_device();
+  if (d.device < 0 || d.sms <= 0) return CONVROT_ERR_CUDA;
+  const int group = a.q_heads / a.kv_heads;
+  a.head_chunks = (group + 127) / 128;
+  a.tile_heads = (group + a.head_chunks - 1) / a.head_chunks;
+  a.tile_tokens = 128 / a.tile_heads;
+  CUtensorMap mq, mk, mv;
+  if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, D, a.q_stride, a.tile_heads, a.tile_tokens))
+    return CONVROT_ERR_CUDA;
+  mk = mv = mq;  // without keys nothing is fetched through them
+  if (a.kv_tokens > 0 && (!make_heads_map(&mk, a.k, a.kv_tokens, a.kv_heads, D, a.k_stride, 1, PROMPT_KEYS) ||
+                          !make_heads_map(&mv, a.v, a.kv_tokens, a.kv_heads, D, a.v_stride, 1, PROMPT_KEYS)))
+    return CONVROT_ERR_CUDA;
+  auto k = prompt_kernel<D>;
+  constexpr int smem = PromptSmem<D>::TOTAL;
+  static std::atomic<bool> configured[64];
+  if (!configured[d.device].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+      return CONVROT_ERR_CUDA;
+    configured[d.device].store(true, std::memory_order_release);
+  }
+  // the lengths are on the device: at most this many units
+  const int64_t units = (static_cast<int64_t>(a.tokens) / (2 * a.tile_tokens) + std::min(a.seqs, a.tokens)) *
+                        a.kv_heads * a.head_chunks;
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, d.sms));
+  return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -132,9 +178,7 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
   a.kv_heads = kv_heads;
   a.scale_log2 = scale * LOG2E;
   a.causal = causal != 0;
-  const int64_t warps = static_cast<int64_t>(tokens) * q_heads;
-  return launch_pdl(head_dim == 128 ? prompt_rows_kernel<128> : prompt_rows_kernel<64>,
-                    dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, as_cuda(stream), 1, a);
+  return head_dim == 128 ? run_prompt<128>(a, as_cuda(stream)) : run_prompt<64>(a, as_cuda(stream));
 }
 
 size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {

@@ -1,4 +1,33 @@
-// Attention over whole prompts, packed one after another.
+// Attention over whole prompts, packed one after another, on the 5th-generation
+// tensor cores.
+//
+//   O_i = sum_j softmax_j(scale q_i . k_j) v_j  over the keys row i sees
+//
+// One pass over the keys with a running reference m and sum l per row:
+//   P = exp2(c S - c m), S = Q K^T, c = scale log2(e);  l += sum P;  O += P V
+// m is a score that was the row's maximum at some point, not at every point:
+// it is raised (and O and l multiplied by exp2(c (m_old - m_new))) only when a
+// tile's maximum is more than 2^8 above it, so P stays below 256, O and l in
+// fp32 lose nothing, and the accumulator is almost never re-read.  P is rounded
+// to bf16 for its product with V (half a step, 2^-8 of a probability, as the
+// result itself is); l is summed from the unrounded values.
+//
+// Work split.  A unit is 2 x 128 query rows of one key/value head: a row is
+// (token, query head of the group), so a group's heads share every key and
+// value tile and a short prompt still fills the matrix unit.  A persistent CTA
+// per SM takes units by a fixed order, the longest key ranges first and every
+// second round backwards.  Warps 0-3 and 4-7 each own one 128-row tile (a
+// thread owns a row; no exchange between threads), warp 8 fetches by TMA and
+// announces units, warp 9 issues the matrix products.  While one tile's
+// softmax runs, the tensor core works on the other's S or O.
+//
+// Tensor memory: S0, S1 (128 columns each; P overwrites its own S), O0, O1.
+// Shared memory: the two Q tiles and a ring of K and V tiles (128 keys).
+//
+// A probability of zero times an infinite or NaN value is NaN in the matrix
+// unit.  Such a value may sit in a masked place (a later token, the next
+// sequence of the pack, memory behind the last one), so a row whose result
+// holds a NaN is computed again by attention_row over its visible keys alone.
 #pragma once
 
 #include "attn_row.cuh"
@@ -11,34 +40,535 @@ struct PromptArgs {
   uint16_t* o;
   const int32_t *cu_q, *cu_k;                      // [seqs + 1]
   int tokens, kv_tokens, seqs, q_heads, kv_heads;
+  int tile_heads;                                  // query heads of one tile (<= 128)
+  int tile_tokens;                                 // tokens of one tile: 128 / tile_heads
+  int head_chunks;                                 // tiles side by side for one group
   float scale_log2;                                // scale * log2(e)
   int causal;
 };
 
-// One warp per (token, head).
+constexpr int PROMPT_KEYS = 128;     // keys per tile
+constexpr int PROMPT_THREADS = 384;  // 2 softmax warpgroups, 1 of fetch + issue
+constexpr unsigned SITE_ATTN = 9;    // wait sites SITE_ATTN .. SITE_ATTN + 5
+
 template <int D>
-__global__ void __launch_bounds__(128) prompt_rows_kernel(const PromptArgs a) {
+struct PromptSmem {
+  static constexpr int TILE = 128 * D * 2;                // bytes of a Q, K or V tile
+  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int RING = 2 * TILE;
+  static constexpr int BARS = RING + STAGES * TILE;
+  static constexpr int N_BARS = 2 * STAGES + 15;
+  static constexpr int INFO = BARS + 8 * N_BARS;
+  static constexpr int MISC = INFO + 2 * 48;
+  static constexpr int TOTAL = MISC + 16 + 1024;          // + alignment of the first tile
+};
+
+// One unit of work as the fetching warp announces it.
+struct PromptUnit {
+  int tok0, ntok;  // first query row of the unit (token) and its tokens
+  int k0, lk;      // the sequence's keys
+  int lim0;        // keys the first token sees (causal; may be negative)
+  int head0;       // first query head
+  int nheads;      // query heads of the unit
+  int kvh;
+  int n[2];        // key tiles of the two row tiles; n[0] = -1: no more units
+  int pad[2];
+};
+static_assert(sizeof(PromptUnit) == 48, "unit layout");
+
+// ---------------------------------------------------------------- tcgen05 pieces
+// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16 bf16.
+__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
+                                            uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Shared-memory descriptor of an operand whose N (or M) elements are contiguous:
+// 64-element (128-byte, swizzled) lines, one per K row; 8 K rows 1024 bytes
+// apart, the next 64 elements `next64` bytes on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t next64) {
+  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(next64 >> 4) << 16) |
+         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
+
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+  return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
+
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
+// Bounded wait that starts its limit anew while a softmax warp of this CTA is
+// recomputing rows (*busy != 0): that work is finite, but may be long.
+__device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, volatile int* abort,
+                                            volatile int* busy, unsigned site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  long long start = clock64();
+  for (uint32_t it = 1;; ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0) {
+      if (*abort) return false;
+      if (*busy) {
+        start = clock64();
+      } else if (clock64() - start > WAIT_LIMIT_CYCLES) {
+        report_error(ERR_WAIT_TIMEOUT | ((site & 0xFFu) << 8));
+        *abort = 1;
+        return false;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------- units
+// Blocks of 2 * tile_tokens tokens of sequence i; 0 (and an error) if its
+// offsets leave the tensors.
+__device__ __forceinline__ int prompt_blocks(const PromptArgs& a, int i) {
+  const int q0 = a.cu_q[i], lq = a.cu_q[i + 1] - q0, k0 = a.cu_k[i], lk = a.cu_k[i + 1] - k0;
+  if (q0 < 0 || lq < 0 || q0 > a.tokens || lq > a.tokens - q0 || k0 < 0 || lk < 0 || k0 > a.kv_tokens ||
+      lk > a.kv_tokens - k0) {
+    report_error(ERR_BAD_ARGUMENT);
+    return 0;
+  }
+  return (lq + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
+}
+
+// The whole warp looks for the sequence that holds block `block` of the pack
+// (block < total); returns its index and the block's index inside it.
+__device__ __forceinline__ int prompt_find(const PromptArgs& a, int block, int& inside) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int i0 = 0; i0 < a.seqs; i0 += 32) {
+    int n = i0 + lane < a.seqs ? prompt_blocks(a, i0 + lane) : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + sum > block);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      inside = block - before - __shfl_sync(0xFFFFFFFFu, sum - n, l);
+      return i0 + l;
+    }
+    before += __shfl_sync(0xFFFFFFFFu, sum, 31);
+  }
+  inside = 0;
+  return -1;
+}
+
+__device__ __forceinline__ int prompt_total(const PromptArgs& a) {
+  int n = 0;
+  for (int i = threadIdx.x & 31; i < a.seqs; i += 32) n += prompt_blocks(a, i);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
+  return n;
+}
+
+// Keys that token `i` of the unit sees.
+__device__ __forceinline__ int prompt_limit(const PromptUnit& u, int causal, int i) {
+  return causal ? max(0, min(u.lk, u.lim0 + i)) : u.lk;
+}
+
+// ---------------------------------------------------------------- the kernel
+template <int D>
+__global__ void __launch_bounds__(PROMPT_THREADS, 1)
+prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+              const __grid_constant__ CUtensorMap tm_v, const PromptArgs a) {
+  using SM = PromptSmem<D>;
+  constexpr int S = SM::STAGES;
+  constexpr int HALVES = D / 64;         // 128-byte lines per row
+  constexpr uint32_t TM_S = 0, TM_O = 256;
+  extern __shared__ uint8_t raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
+  uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::BARS);
+  uint64_t *kv_full = bars, *kv_empty = bars + S, *q_full = bars + 2 * S, *q_empty = q_full + 2,
+           *s_full = q_full + 4, *p_full = q_full + 6, *o_done = q_full + 8, *info_full = q_full + 10,
+           *info_empty = q_full + 12, *drain = q_full + 14;
+  PromptUnit* info = reinterpret_cast<PromptUnit*>(smem + SM::INFO);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::MISC);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  volatile int* busy = reinterpret_cast<volatile int*>(tmem_slot + 2);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
   pdl_launch_dependents();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < S; ++i) {
+      mbar_init(&kv_full[i], 1);
+      mbar_init(&kv_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&q_full[i], 1);
+      mbar_init(&q_empty[i], 1);
+      mbar_init(&s_full[i], 1);
+      mbar_init(&p_full[i], 4);
+      mbar_init(&o_done[i], 1);
+      mbar_init(&info_full[i], 1);
+      mbar_init(&info_empty[i], 9);  // the issuing warp and the eight softmax warps
+    }
+    mbar_init(drain, 1);
+    *abort_flag = 0;
+    *busy = 0;
+    fence_barrier_init();
+  }
+  if (warp == 8) {
+    tmem_alloc(tmem_slot, 512);
+    tmem_relinquish();
+    if (lane == 0) {
+      tma_prefetch_desc(&tm_q);
+      tma_prefetch_desc(&tm_k);
+      tma_prefetch_desc(&tm_v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
   pdl_wait();
-  const int64_t w = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-  const int t = static_cast<int>(w / a.q_heads), h = static_cast<int>(w - static_cast<int64_t>(t) * a.q_heads);
-  if (t >= a.tokens || t >= a.cu_q[a.seqs] || t < a.cu_q[0]) return;
-  int lo = 0, hi = a.seqs;  // cu_q[lo] <= t < cu_q[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.cu_q[mid] <= t) lo = mid; else hi = mid;
+
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    if (warp == 8) {
+      // ------------------------------------------------------ fetch
+      const int total = prompt_total(a);
+      const int heads = a.kv_heads * a.head_chunks;
+      const int64_t units = static_cast<int64_t>(total) * heads;
+      const int group = a.q_heads / a.kv_heads;
+      uint32_t it = 0, q_use[2] = {0, 0}, n_info = 0;
+      bool ok = true;
+      for (int64_t round = 0; ok; ++round) {
+        const int64_t at = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        if (at >= units && round * gridDim.x >= units) break;
+        if (at >= units) continue;
+        // the blocks with the most keys first, a block's heads side by side
+        const int block = total - 1 - static_cast<int>(at / heads);
+        const int head = static_cast<int>(at % heads);
+        int inside;
+        const int seq = prompt_find(a, block, inside);
+        PromptUnit u;
+        u.kvh = head / a.head_chunks;
+        const int chunk = head % a.head_chunks;
+        u.head0 = u.kvh * group + chunk * a.tile_heads;
+        u.nheads = min(a.tile_heads, group - chunk * a.tile_heads);
+        const int q0 = a.cu_q[seq], lq = a.cu_q[seq + 1] - q0, first = inside * 2 * a.tile_tokens;
+        u.tok0 = q0 + first;
+        u.ntok = min(2 * a.tile_tokens, lq - first);
+        u.k0 = a.cu_k[seq];
+        u.lk = a.cu_k[seq + 1] - u.k0;
+        u.lim0 = first + 1 + u.lk - lq;
+        u.n[0] = (prompt_limit(u, a.causal, min(u.ntok, a.tile_tokens) - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS;
+        u.n[1] = u.ntok > a.tile_tokens ? (prompt_limit(u, a.causal, u.ntok - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
+        u.pad[0] = u.pad[1] = 0;
+        if (lane == 0) {
+          const uint32_t slot = n_info & 1u;
+          ok = prompt_wait(&info_empty[slot], ((n_info >> 1) & 1u) ^ 1u, abort_flag, busy, SITE_ATTN);
+          if (ok) {
+            info[slot] = u;
+            mbar_arrive(&info_full[slot]);
+          }
+          auto load_q = [&](int w) {
+            if (!ok || u.n[w] == 0) return;
+            ok = prompt_wait(&q_empty[w], (q_use[w] & 1u) ^ 1u, abort_flag, busy, SITE_ATTN);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&q_full[w], a.tile_heads * a.tile_tokens * D * 2);
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_3d(smem + w * SM::TILE + h * 16384, &tm_q, &q_full[w], h * 64, u.head0,
+                          u.tok0 + w * a.tile_tokens);
+            ++q_use[w];
+          };
+          auto load_kv = [&](const CUtensorMap* map, int j) {
+            if (!ok) return;
+            const uint32_t s = it % S;
+            ok = prompt_wait(&kv_empty[s], ((it / S) & 1u) ^ 1u, abort_flag, busy, SITE_ATTN + 1);
+            if (!ok) return;
+            mbar_arrive_expect_tx(&kv_full[s], SM::TILE);
+            for (int h = 0; h < HALVES; ++h)
+              tma_load_3d(smem + SM::RING + s * SM::TILE + h * 16384, map, &kv_full[s], h * 64, u.kvh,
+                          u.k0 + j * PROMPT_KEYS);
+            ++it;
+          };
+          const int n = max(u.n[0], u.n[1]);
+          load_q(0);
+          if (n > 0) load_kv(&tm_k, 0);
+          load_q(1);
+          for (int j = 0; j < n && ok; ++j) {
+            load_kv(&tm_v, j);
+            if (j + 1 < n) load_kv(&tm_k, j + 1);
+          }
+        }
+        ++n_info;
+        ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+      }
+      if (lane == 0) {
+        if (ok && prompt_wait(&info_empty[n_info & 1u], ((n_info >> 1) & 1u) ^ 1u, abort_flag, busy, SITE_ATTN)) {
+          info[n_info & 1u].n[0] = -1;
+          mbar_arrive(&info_full[n_info & 1u]);
+        }
+        // no copy may still be landing in shared memory when the CTA exits
+        int never = 0;
+        for (uint32_t j = it > S ? it - S : 0u; j < it; ++j) mbar_wait(&kv_full[j % S], (j / S) & 1u, &never, SITE_DRAIN);
+        for (int w = 0; w < 2; ++w)
+          if (q_use[w]) mbar_wait(&q_full[w], (q_use[w] - 1) & 1u, &never, SITE_DRAIN);
+      }
+    } else if (warp == 9 && lane == 0) {
+      // ------------------------------------------------------ matrix products
+      const uint32_t idesc_s = idesc_bf16_f32(128, 128);
+      const uint32_t idesc_o = idesc_bf16_f32(128, D) | IDESC_B_MN_MAJOR;
+      const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + SM::RING);
+      uint32_t it = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
+      auto scores = [&](int w, uint32_t stage) {
+        const uint64_t qd = sw128_kmajor_desc(q_addr + w * SM::TILE), kd = sw128_kmajor_desc(ring + stage * SM::TILE);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          // 32 bytes along a 128-byte line; the second half of the row is 16 KB on
+          const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * 2;
+          mma_bf16_ss(tmem + TM_S + w * 128, qd + off, kd + off, idesc_s, k > 0);
+        }
+        mma_commit(&s_full[w]);
+      };
+      auto values = [&](int w, uint32_t stage, bool accumulate) {
+        const uint32_t base = ring + stage * SM::TILE;
+#pragma unroll
+        for (int k = 0; k < PROMPT_KEYS / 16; ++k)
+          mma_bf16_ts(tmem + TM_O + w * 128, tmem + TM_S + w * 128 + k * 8,
+                      sw128_mnmajor_desc(base + k * 2048, 16384), idesc_o, accumulate || k > 0);
+        mma_commit(&o_done[w]);
+      };
+      bool ok = true;
+      for (uint32_t n_info = 0; ok; ++n_info) {
+        ok = prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 2);
+        if (!ok) break;
+        const int n0 = info[n_info & 1u].n[0], n1 = info[n_info & 1u].n[1];
+        if (n0 < 0) break;
+        mbar_arrive(&info_empty[n_info & 1u]);
+        const int n = max(n0, n1), nw[2] = {n0, n1};
+        if (n == 0) continue;
+        ok = prompt_wait(&kv_full[it % S], (it / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (!ok || nw[w] == 0) continue;
+          ok = prompt_wait(&q_full[w], q_use[w] & 1u, abort_flag, busy, SITE_ATTN + 2);
+          ++q_use[w];
+          if (!ok) continue;
+          tc_fence_after();
+          scores(w, it % S);
+          if (nw[w] == 1) mma_commit(&q_empty[w]);
+        }
+        if (!ok) break;
+        mma_commit(&kv_empty[it % S]);
+        ++it;
+        for (int j = 0; j < n && ok; ++j) {
+          const uint32_t sv = it % S, sk = (it + 1) % S;
+          ok = prompt_wait(&kv_full[sv], (it / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+          bool have_k = false;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (!ok || j >= nw[w]) continue;
+            ok = prompt_wait(&p_full[w], p_use[w] & 1u, abort_flag, busy, SITE_ATTN + 3);
+            ++p_use[w];
+            if (!ok) continue;
+            tc_fence_after();
+            values(w, sv, j > 0);
+            if (j + 1 < nw[w]) {
+              if (!have_k) ok = prompt_wait(&kv_full[sk], ((it + 1) / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+              have_k = true;
+              if (!ok) continue;
+              scores(w, sk);
+              if (j + 2 == nw[w]) mma_commit(&q_empty[w]);
+            }
+          }
+          if (!ok) break;
+          mma_commit(&kv_empty[sv]);
+          ++it;
+          if (j + 1 < n) {
+            mma_commit(&kv_empty[sk]);
+            ++it;
+          }
+        }
+      }
+      // every product issued must be complete before tensor memory is released
+      mma_commit(drain);
+      int never = 0;
+      mbar_wait(drain, 0u, &never, SITE_DRAIN);
+    }
+  } else {
+    // -------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    const int w = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;
+    const int tok = row / a.tile_heads, hd = row - tok * a.tile_heads;
+    const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const uint32_t t_s = tmem + lanes + TM_S + w * 128, t_o = tmem + lanes + TM_O + w * 128;
+    const float c = a.scale_log2, raise = 8.f / c;
+    uint32_t s_use = 0;  // S tiles taken so far = O products awaited or not
+    for (uint32_t n_info = 0;; ++n_info) {
+      if (!prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 4)) break;
+      const PromptUnit u = info[n_info & 1u];
+      __syncwarp();
+      if (u.n[0] < 0) break;
+      if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
+      const int i = w * a.tile_tokens + tok;  // token of the unit
+      const bool valid = tok < a.tile_tokens && i < u.ntok && hd < u.nheads;
+      // rows that are not stored mask nothing
+      const int lim = valid ? prompt_limit(u, a.causal, i) : 1 << 30;
+      const int warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
+      float m = -INFINITY, l = 0.f;
+      bool ok = true;
+      for (int j = 0; j < u.n[w]; ++j, ++s_use) {
+        ok = prompt_wait(&s_full[w], s_use & 1u, abort_flag, busy, SITE_ATTN + 4);
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tmem_ld_32x32b_x32(t_s + 32 * x, s[x]);
+        tmem_ld_wait();
+        if ((j + 1) * PROMPT_KEYS > warp_lim) {
+          const int rel = lim - j * PROMPT_KEYS;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * x + e >= rel) s[x][e] = 0xFF800000u;  // -inf
+        }
+        float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int e = 0; e < 32; ++e)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], __uint_as_float(s[x][e]));
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+        if (j == 0) {
+          m = high;
+        } else if (__any_sync(0xFFFFFFFFu, high > m + raise)) {
+          const float m_new = high > m + raise ? high : m;
+          const float f = m_new == m ? 1.f : ex2((m - m_new) * c);
+          m = m_new;
+          l *= f;
+          ok = prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int x = 0; x < D / 32; ++x) {
+            uint32_t o[32];
+            tmem_ld_32x32b_x32(t_o + 32 * x, o);
+            tmem_ld_wait();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_32x32b_x32(t_o + 32 * x, o);
+          }
+        }
+        const float shift = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t c2 = pack2(c, c), shift2 = pack2(shift, shift);
+        uint64_t sum2[2] = {0, 0};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          uint32_t p[32];
+#pragma unroll
+          for (int e = 0; e < 32; ++e) {
+            const uint32_t* in = &s[2 * x + e / 16][(2 * e) % 32];
+            float lo, hi;
+            unpack2(fma2(pack2(__uint_as_float(in[0]), __uint_as_float(in[1])), c2, shift2), lo, hi);
+            lo = ex2(lo);
+            hi = ex2(hi);
+            sum2[e & 1] = add2(sum2[e & 1], pack2(lo, hi));
+            p[e] = cvt_bf16x2(lo, hi);
+          }
+          tmem_st_32x32b_x32(t_s + 32 * x, p);
+        }
+        float s0, s1;
+        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[w]);
+      }
+      if (!ok) break;
+      // ---- result
+      uint16_t* out = a.o + static_cast<int64_t>(u.tok0 + i) * a.o_stride + static_cast<int64_t>(u.head0 + hd) * D;
+      bool bad = false;
+      if (u.n[w] > 0) {
+        if (!prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
+        tc_fence_after();
+        const float inv = lim > 0 ? 1.f / l : 0.f;
+#pragma unroll
+        for (int x = 0; x < D / 32; ++x) {
+          uint32_t o[32];
+          tmem_ld_32x32b_x32(t_o + 32 * x, o);
+          tmem_ld_wait();
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y) {
+              f[y] = lim > 0 ? __uint_as_float(o[e + y]) * inv : 0.f;
+              bad |= f[y] != f[y];
+            }
+            if (valid)
+              *reinterpret_cast<uint4*>(out + 32 * x + e) =
+                  make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
+                             cvt_bf16x2(f[6], f[7]));
+          }
+        }
+        tc_fence_before();
+      } else if (valid) {
+#pragma unroll
+        for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(out + e) = make_uint4(0, 0, 0, 0);
+      }
+      unsigned again = __ballot_sync(0xFFFFFFFFu, bad && valid);
+      if (again) {
+        if (lane == 0) atomicAdd(const_cast<int*>(busy), 1);
+        while (again) {
+          const int r = __ffs(again) - 1;
+          again &= again - 1;
+          const int ri = __shfl_sync(0xFFFFFFFFu, i, r), rh = __shfl_sync(0xFFFFFFFFu, hd, r);
+          const int64_t t = u.tok0 + ri;
+          const int64_t h = static_cast<int64_t>(u.head0 + rh) * D, kh = static_cast<int64_t>(u.kvh) * D;
+          attention_row<D>(a.q + t * a.q_stride + h, a.k + u.k0 * a.k_stride + kh, a.k_stride,
+                           a.v + u.k0 * a.v_stride + kh, a.v_stride, prompt_limit(u, a.causal, ri), c,
+                           a.o + t * a.o_stride + h);
+        }
+        __syncwarp();
+        if (lane == 0) atomicSub(const_cast<int*>(busy), 1);
+      }
+    }
   }
-  const int q0 = a.cu_q[lo], lq = a.cu_q[lo + 1] - q0, k0 = a.cu_k[lo], lk = a.cu_k[lo + 1] - k0;
-  if (q0 < 0 || lq > a.tokens - q0 || k0 < 0 || lk < 0 || lk > a.kv_tokens - k0) {
-    if ((threadIdx.x & 31) == 0) report_error(ERR_BAD_ARGUMENT);
-    return;
-  }
-  const int n = a.causal ? max(0, min(lk, t - q0 + 1 + lk - lq)) : lk;
-  const int kh = h / (a.q_heads / a.kv_heads);
-  attention_row<D>(a.q + t * a.q_stride + static_cast<int64_t>(h) * D,
-                   a.k + k0 * a.k_stride + static_cast<int64_t>(kh) * D, a.k_stride,
-                   a.v + k0 * a.v_stride + static_cast<int64_t>(kh) * D, a.v_stride, n, a.scale_log2,
-                   a.o + t * a.o_stride + static_cast<int64_t>(h) * D);
+  __syncthreads();
+  if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
 }  // namespace convrot

@@ -426,8 +426,9 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  * lens       int32 [seqs]  in   0 .. table_cols * page_size
  * out        bf16 [seqs, q_heads, D]  out
  * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte
- *            aligned, zero-filled before its first use; every call leaves it
- *            fit for the next.  Calls that overlap on the GPU need one each.
+ *            aligned, zero-filled before its first use; every call that
+ *            completes leaves it zero, so the linears may share it.  Calls that
+ *            overlap on the GPU need one each.
  */
 size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim);
 convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seqs, int q_heads, int kv_heads,

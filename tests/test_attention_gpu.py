@@ -548,3 +548,12 @@ def test_captured_append_and_prompt(cr):
     check_append(c, before, qo, ko)
     ref_o, tol = ref.packed_attention(f64(q), f64(k), f64(v), [0, 130, 260], [0, 130, 260], 64 ** -0.5, True)
     within(f64(o), ref_o, tol, "replayed prompt")
+
+
+def test_decode_leaves_its_workspace_zero(cr):
+    """The linears' contract: a Workspace may serve both."""
+    ws = cr.Workspace()
+    for lens in ([5000, 3], [64 * 7] * 40, [1]):
+        c = decode_case(50, lens, 8, 2, 128, 16, False)
+        check_decode(cr, c, lens, workspace=ws)
+        assert not ws.buf.any()

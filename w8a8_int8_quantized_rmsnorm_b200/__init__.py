@@ -549,6 +549,8 @@ def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_sc
                      k_scale=k_scale, v_scale=v_scale, out=out)
     if out is None:
         out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
+    if workspace is None and torch.cuda.is_current_stream_capturing():
+        workspace = Workspace(dev.index)  # a graph's own: graphs may be replayed at the same time
     ws, wn = _workspace(dev, convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D), workspace)
     _check("convrot_attention_decode", lib().convrot_attention_decode(
         _ptr(q), _row_stride(q), B, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages,

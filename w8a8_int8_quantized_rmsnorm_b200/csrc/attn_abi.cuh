@@ -81,6 +81,60 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, a);
 }
 
+// Heads of a decode unit: up to eight together, else sixteen at a time.
+int decode_unit_heads(int q_heads, int kv_heads) { return std::min(q_heads / kv_heads, 16); }
+
+constexpr int kDecodeSmem = 228 * 1024 / 2 - 1024;  // two CTAs per SM
+
+int decode_grid(const DeviceInfo& d) { return 2 * d.sms; }
+
+size_t decode_counter_bytes(int grid) { return (static_cast<size_t>(grid) * 4 + 255) / 256 * 256; }
+
+size_t decode_ws_bytes(int grid, int heads, int D) {
+  return decode_counter_bytes(grid) + static_cast<size_t>(grid) * 2 * decode_part_floats(heads, D) * sizeof(float);
+}
+
+// A paged cache as a 3-D map (bytes or elements of a line, row, line of the
+// row): lines of 128 bytes (64 where a row is no longer), rows of all pages
+// and heads one after another.
+bool make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, bool int8, int box_rows) {
+  EncodeTiledFn fn = encode_fn();
+  if (!fn) return false;
+  const int esz = int8 ? 1 : 2, line = D * esz >= 128 ? 128 : 64, halves = D * esz / line;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(line / esz), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(halves)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * esz, static_cast<cuuint64_t>(line)};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(line / esz), static_cast<cuuint32_t>(box_rows),
+                             static_cast<cuuint32_t>(halves)};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  return fn(map, int8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+            dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            line == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int D, bool I8, int NQ>
+convrot_status run_decode(const DecodeArgs& args, const void* k_cache, const void* v_cache, int grid, cudaStream_t st) {
+  using SM = DecodeSmem<D, I8, NQ>;
+  DecodeArgs a = args;
+  const DeviceInfo d = current_device();
+  const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(a.pages) * a.kv_heads * a.page_size);
+  CUtensorMap mk, mv;
+  if (!make_cache_map(&mk, k_cache, rows, D, I8, a.box_rows) || !make_cache_map(&mv, v_cache, rows, D, I8, a.box_rows))
+    return CONVROT_ERR_CUDA;
+  a.stages = DECODE_MAX_STAGES;
+  while (a.stages > 2 && SM::total(a.stages, a.chunk_heads) > kDecodeSmem) --a.stages;
+  const int smem = SM::total(a.stages, a.chunk_heads);
+  auto k = decode_kernel<D, I8, NQ>;
+  static std::atomic<bool> configured[64];
+  if (!configured[d.device].load(std::memory_order_acquire)) {
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmem) != cudaSuccess)
+      return CONVROT_ERR_CUDA;
+    configured[d.device].store(true, std::memory_order_release);
+  }
+  return launch_pdl(k, dim3(grid), dim3(DECODE_THREADS), smem, st, 1, mk, mv, a);
+}
+
 }  // namespace
 
 extern "C" {
@@ -182,9 +236,10 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
 }
 
 size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim) {
-  (void)seqs;
-  if (!heads_ok(q_heads, kv_heads) || (head_dim != 64 && head_dim != 128)) return 0;
-  return 0;
+  if (seqs <= 0 || !heads_ok(q_heads, kv_heads) || (head_dim != 64 && head_dim != 128)) return 0;
+  const DeviceInfo d = current_device();
+  if (d.device < 0 || d.sms <= 0) return 0;
+  return decode_ws_bytes(decode_grid(d), decode_unit_heads(q_heads, kv_heads), head_dim);
 }
 
 convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seqs, int q_heads, int kv_heads,
@@ -193,8 +248,6 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
                                         const int32_t* table, int64_t table_stride, int table_cols,
                                         const int32_t* lens, float scale, void* out, int64_t out_stride,
                                         void* workspace, size_t workspace_bytes, convrot_stream_t stream) {
-  (void)workspace;
-  (void)workspace_bytes;
   if (seqs < 0 || !heads_ok(q_heads, kv_heads)) return CONVROT_ERR_SHAPE;
   if (head_dim != 64 && head_dim != 128) return CONVROT_ERR_UNSUPPORTED;
   if (seqs > (1 << 24) || pages < 0 || page_size < 1 || page_size > kMaxPage || page_size % 16 || table_cols < 0)
@@ -205,8 +258,9 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
     return CONVROT_ERR_SHAPE;
   if (seqs == 0) return CONVROT_OK;
   if (!q || !out || !lens || !k_scale != !v_scale) return CONVROT_ERR_NULL;
-  if ((pages > 0 && (!k_cache || !v_cache)) || (table_cols > 0 && !table)) return CONVROT_ERR_NULL;
-  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+  if (!k_cache || !v_cache || (table_cols > 0 && !table)) return CONVROT_ERR_NULL;
+  if (static_cast<int64_t>(pages) * kv_heads * page_size > 0x7FFFFFFF) return CONVROT_ERR_UNSUPPORTED;  // rows of a TMA map
+  if (!aligned(workspace, 256) || !aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(table, 4) || !aligned(lens, 4))
     return CONVROT_ERR_ALIGN;
   DecodeArgs a{};
@@ -214,8 +268,6 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   a.q_stride = q_stride;
   a.o_stride = out_stride;
   a.o = static_cast<uint16_t*>(out);
-  a.k_cache = k_cache;
-  a.v_cache = v_cache;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
   a.table = table;
@@ -228,11 +280,26 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   a.page_size = page_size;
   a.table_cols = table_cols;
   a.scale_log2 = scale * LOG2E;
-  const int64_t warps = static_cast<int64_t>(seqs) * q_heads;
-  const bool i8 = k_scale != nullptr;
-  auto kern = head_dim == 128 ? (i8 ? decode_rows_kernel<128, true> : decode_rows_kernel<128, false>)
-                              : (i8 ? decode_rows_kernel<64, true> : decode_rows_kernel<64, false>);
-  return launch_pdl(kern, dim3(static_cast<unsigned>((warps + 3) / 4)), dim3(128), 0, as_cuda(stream), 1, a);
+  const DeviceInfo d = current_device();
+  if (d.device < 0 || d.sms <= 0) return CONVROT_ERR_CUDA;
+  const int group = q_heads / kv_heads;
+  a.chunk_heads = decode_unit_heads(q_heads, kv_heads);
+  a.chunks = (group + a.chunk_heads - 1) / a.chunk_heads;
+  a.box_rows = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
+  int grid = decode_grid(d);
+  if (!workspace || workspace_bytes < decode_ws_bytes(grid, a.chunk_heads, head_dim)) return CONVROT_ERR_WORKSPACE;
+  a.counters = static_cast<unsigned*>(workspace);
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_counter_bytes(grid));
+  // no more CTAs than blocks there can be
+  const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + DECODE_KEYS - 1) / DECODE_KEYS);
+  grid = static_cast<int>(std::min<int64_t>(grid, most * seqs * kv_heads * a.chunks));
+  const bool i8 = k_scale != nullptr, wide = a.chunk_heads > 8;
+  cudaStream_t st = as_cuda(stream);
+#define CONVROT_DECODE(D)                                                                                     \
+  (i8 ? (wide ? run_decode<D, true, 16>(a, k_cache, v_cache, grid, st) : run_decode<D, true, 8>(a, k_cache, v_cache, grid, st)) \
+      : (wide ? run_decode<D, false, 16>(a, k_cache, v_cache, grid, st) : run_decode<D, false, 8>(a, k_cache, v_cache, grid, st)))
+  return head_dim == 128 ? CONVROT_DECODE(128) : CONVROT_DECODE(64);
+#undef CONVROT_DECODE
 }
 
 }  // extern "C"

@@ -84,9 +84,9 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
 // Heads of a decode unit: up to eight together, else sixteen at a time.
 int decode_unit_heads(int q_heads, int kv_heads) { return std::min(q_heads / kv_heads, 16); }
 
-constexpr int kDecodeSmem = 228 * 1024 / 2 - 1024;  // two CTAs per SM
+constexpr int kDecodeCtas = 3;  // most CTAs per SM of any decode kernel
 
-int decode_grid(const DeviceInfo& d) { return 2 * d.sms; }
+int decode_grid(const DeviceInfo& d) { return kDecodeCtas * d.sms; }
 
 size_t decode_counter_bytes(int grid) { return (static_cast<size_t>(grid) * 4 + 255) / 256 * 256; }
 
@@ -114,8 +114,11 @@ bool make_cache_map(CUtensorMap* map, const void* base, int64_t rows, int D, boo
 }
 
 template <int D, bool I8, int NQ>
-convrot_status run_decode(const DecodeArgs& args, const void* k_cache, const void* v_cache, int grid, cudaStream_t st) {
+convrot_status run_decode(const DecodeArgs& args, const void* k_cache, const void* v_cache, int64_t blocks,
+                          cudaStream_t st) {
   using SM = DecodeSmem<D, I8, NQ>;
+  static_assert(SM::CTAS <= kDecodeCtas, "the workspace is sized for kDecodeCtas");
+  constexpr int budget = 228 * 1024 / SM::CTAS - 1024;
   DecodeArgs a = args;
   const DeviceInfo d = current_device();
   const int64_t rows = std::max<int64_t>(1, static_cast<int64_t>(a.pages) * a.kv_heads * a.page_size);
@@ -123,15 +126,16 @@ convrot_status run_decode(const DecodeArgs& args, const void* k_cache, const voi
   if (!make_cache_map(&mk, k_cache, rows, D, I8, a.box_rows) || !make_cache_map(&mv, v_cache, rows, D, I8, a.box_rows))
     return CONVROT_ERR_CUDA;
   a.stages = DECODE_MAX_STAGES;
-  while (a.stages > 2 && SM::total(a.stages, a.chunk_heads) > kDecodeSmem) --a.stages;
+  while (a.stages > 2 && SM::total(a.stages, a.chunk_heads) > budget) --a.stages;
   const int smem = SM::total(a.stages, a.chunk_heads);
   auto k = decode_kernel<D, I8, NQ>;
   static std::atomic<bool> configured[64];
   if (!configured[d.device].load(std::memory_order_acquire)) {
-    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kDecodeSmem) != cudaSuccess)
+    if (cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, budget) != cudaSuccess)
       return CONVROT_ERR_CUDA;
     configured[d.device].store(true, std::memory_order_release);
   }
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(SM::CTAS * d.sms, blocks));
   return launch_pdl(k, dim3(grid), dim3(DECODE_THREADS), smem, st, 1, mk, mv, a);
 }
 
@@ -286,18 +290,18 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   a.chunk_heads = decode_unit_heads(q_heads, kv_heads);
   a.chunks = (group + a.chunk_heads - 1) / a.chunk_heads;
   a.box_rows = page_size % 64 == 0 ? 64 : page_size % 32 == 0 ? 32 : 16;
-  int grid = decode_grid(d);
+  const int grid = decode_grid(d);
   if (!workspace || workspace_bytes < decode_ws_bytes(grid, a.chunk_heads, head_dim)) return CONVROT_ERR_WORKSPACE;
   a.counters = static_cast<unsigned*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_counter_bytes(grid));
   // no more CTAs than blocks there can be
   const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + DECODE_KEYS - 1) / DECODE_KEYS);
-  grid = static_cast<int>(std::min<int64_t>(grid, most * seqs * kv_heads * a.chunks));
+  const int64_t blocks = most * seqs * kv_heads * a.chunks;
   const bool i8 = k_scale != nullptr, wide = a.chunk_heads > 8;
   cudaStream_t st = as_cuda(stream);
 #define CONVROT_DECODE(D)                                                                                     \
-  (i8 ? (wide ? run_decode<D, true, 16>(a, k_cache, v_cache, grid, st) : run_decode<D, true, 8>(a, k_cache, v_cache, grid, st)) \
-      : (wide ? run_decode<D, false, 16>(a, k_cache, v_cache, grid, st) : run_decode<D, false, 8>(a, k_cache, v_cache, grid, st)))
+  (i8 ? (wide ? run_decode<D, true, 16>(a, k_cache, v_cache, blocks, st) : run_decode<D, true, 8>(a, k_cache, v_cache, blocks, st)) \
+      : (wide ? run_decode<D, false, 16>(a, k_cache, v_cache, blocks, st) : run_decode<D, false, 8>(a, k_cache, v_cache, blocks, st)))
   return head_dim == 128 ? CONVROT_DECODE(128) : CONVROT_DECODE(64);
 #undef CONVROT_DECODE
 }

@@ -70,6 +70,9 @@ struct DecodeBlock {
 template <int D, bool I8, int NQ>
 struct DecodeSmem {
   static constexpr int ESZ = I8 ? 1 : 2;
+  // CTAs per SM: two keep enough bf16 rows in flight (64 contexts of 1 .. 8192
+  // keys: 0.98 of HBM); int8 rows need more warps, for the conversions
+  static constexpr int CTAS = I8 && NQ == 8 ? 3 : 2;
   static constexpr int TILE = DECODE_KEYS * D * ESZ;
   static constexpr int SLOT = 2 * TILE;                            // K, V
   static constexpr int SIDE = NQ * D * 2 + 2 * DECODE_KEYS * 4;    // Q rows, scales
@@ -105,7 +108,7 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-// Two int8 codes, in the low bytes of the halves of x, as bf16, exactly:
+// Two int8 codes, bytes 0 and 2 of x, as bf16, exactly:
 // (128 + low 7 bits) - (128 or, with the sign bit, 256).
 __device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x) {
   const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, w = (x & 0x00800080u) | 0x43004300u;
@@ -137,7 +140,7 @@ __device__ __forceinline__ int decode_length(const DecodeArgs& a, int b) {
 __device__ __forceinline__ int decode_blocks(int len) { return max(1, (len + DECODE_KEYS - 1) / DECODE_KEYS); }
 
 template <int D, bool I8, int NQ>
-__global__ void __launch_bounds__(DECODE_THREADS, 2)
+__global__ void __launch_bounds__(DECODE_THREADS, DecodeSmem<D, I8, NQ>::CTAS)
 decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const DecodeArgs a) {
   using SM = DecodeSmem<D, I8, NQ>;
   constexpr int ROWB = D * SM::ESZ >= 128 ? 128 : 64;  // bytes of a swizzled line
@@ -213,14 +216,17 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       j = static_cast<int>((at - start) - static_cast<int64_t>(unit) * nb);
     }
     const int boxes = DECODE_KEYS / a.box_rows;
-    // page of this lane's box of block j; -1: not there
+    const unsigned page_size = a.page_size;
+    // page of this lane's box of a block; -1: not there
     auto entry = [&](int b, int blk, int n) -> int {
-      const int64_t key = static_cast<int64_t>(blk) * DECODE_KEYS + lane * a.box_rows;
-      return lane < boxes && key < n ? a.table[b * a.table_stride + key / a.page_size] : -1;
+      const unsigned key = static_cast<unsigned>(blk) * DECODE_KEYS + lane * a.box_rows;
+      return lane < boxes && key < static_cast<unsigned>(n) ? a.table[b * a.table_stride + key / page_size] : -1;
     };
     bool ok = true;
-    uint32_t it = 0;
+    uint32_t it = 0, s = 0, phase = 1;  // slot and the parity its last emptying has
     int page = at < end ? entry(seq, j, len) : -1;
+    const int group = a.q_heads / a.kv_heads;
+    int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
     int next_len = seq + 1 < a.seqs ? decode_length(a, seq + 1) : 0;
     while (at < end && ok) {
       // where the line goes on, and that block's pages
@@ -240,14 +246,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int page2 = more ? entry(seq2, j2, len2) : -1;
       if (seq2 != seq) next_len = seq2 + 1 < a.seqs ? decode_length(a, seq2 + 1) : 0;
 
-      const uint32_t s = it % S;
-      ok = mbar_wait_spin(&empty[s], ((it / S) & 1u) ^ 1u, abort_flag, SITE_DECODE);
+      ok = mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
       if (!ok) break;
-      const int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
-      const int group = a.q_heads / a.kv_heads;
       const int qh = min(heads, group - chunk * heads);
-      const int64_t key0 = static_cast<int64_t>(j) * DECODE_KEYS;
-      const bool wanted = lane < boxes && key0 + lane * a.box_rows < len;
+      const unsigned key = static_cast<unsigned>(j) * DECODE_KEYS + lane * a.box_rows;  // of this lane's box
+      const bool wanted = lane < boxes && key < static_cast<unsigned>(len);
       const bool there = wanted && page >= 0 && page < a.pages;
       if (wanted && !there) report_error(ERR_BAD_ARGUMENT);
       const unsigned mask = __ballot_sync(0xFFFFFFFFu, there);
@@ -257,14 +260,18 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         DecodeBlock m;
         m.seq = seq;
         m.unit = unit;
-        m.left = static_cast<int>(len - key0);
+        m.left = len - j * DECODE_KEYS;
         m.slices = 0;
         for (int x = 0; x < 4; ++x) m.slices |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
         m.first = first;
         m.last = last;
+        m.owner = blockIdx.x;
+        m.n_parts = 1;
         const int64_t item = start + static_cast<int64_t>(unit) * nb;
-        m.owner = static_cast<int>(item / per);
-        m.n_parts = static_cast<int>((item + nb - 1) / per) - m.owner + 1;
+        if (last && (item < begin || item + nb > end)) {  // twice per CTA at most: its two ends
+          m.owner = static_cast<int>(item / per);
+          m.n_parts = static_cast<int>((item + nb - 1) / per) - m.owner + 1;
+        }
         meta[s] = m;
         const uint32_t bytes = __popc(mask) * a.box_rows * (2 * D * SM::ESZ + (I8 ? 8 : 0)) + (first ? qh * D * 2 : 0);
         mbar_arrive_expect_tx(&full[s], bytes);
@@ -275,8 +282,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       }
       __syncwarp();
       if (there) {
-        const int64_t key = key0 + lane * a.box_rows;
-        const int64_t row = (static_cast<int64_t>(page) * a.kv_heads + kvh) * a.page_size + key % a.page_size;
+        const int64_t row = (static_cast<int64_t>(page) * a.kv_heads + kvh) * page_size + key % page_size;
         uint8_t* dst = smem + s * SM::SLOT + lane * a.box_rows * D * SM::ESZ;
         tma_load_3d(dst, &tm_k, &full[s], 0, static_cast<int>(row), 0);
         tma_load_3d(dst + SM::TILE, &tm_v, &full[s], 0, static_cast<int>(row), 0);
@@ -287,7 +293,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
       }
       ++it;
+      if (++s == static_cast<uint32_t>(S)) s = 0, phase ^= 1u;
       ++at;
+      if (unit2 != unit) kvh = unit2 / a.chunks, chunk = unit2 - kvh * a.chunks;
       seq = seq2;
       len = len2;
       nb = nb2;
@@ -296,10 +304,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       start = start2;
       page = page2;
     }
-    ok = ok && mbar_wait_spin(&empty[it % S], ((it / S) & 1u) ^ 1u, abort_flag, SITE_DECODE);
+    ok = ok && mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
     if (ok && lane == 0) {
-      meta[it % S].seq = -1;
-      mbar_arrive(&full[it % S]);
+      meta[s].seq = -1;
+      mbar_arrive(&full[s]);
     }
     // No copy may still be landing in shared memory when the CTA exits.  The
     // slot of the end mark has been taken back already: its copies are in.
@@ -329,9 +337,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int sw = ROWB == 128 ? (row & 7) : ((row >> 1) & 3);
       return base + h * half_step + row * ROWB + ((c ^ sw) << 4);
     };
-    for (uint32_t it = 0;; ++it) {
-      const uint32_t s = it % S;
-      if (!mbar_wait_spin(&full[s], (it / S) & 1u, abort_flag, SITE_DECODE + 2)) break;
+    uint32_t next = 0, phase = 0;
+    for (;;) {
+      const uint32_t s = next;
+      if (!mbar_wait_spin(&full[s], phase, abort_flag, SITE_DECODE + 2)) break;
+      if (++next == static_cast<uint32_t>(S)) next = 0, phase ^= 1u;
       const DecodeBlock b = meta[s];
       if (b.seq < 0) break;
       if (b.first) {
@@ -343,8 +353,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             const uint8_t* p = qs + ((n * 8 + g) * D + k * 16) * 2;
             if (I8) {  // elements 4t .. 4t+3 of the step: see the keys' bytes below
               const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * t);
-              qf[n][k][0] = v.x;
-              qf[n][k][1] = v.y;
+              qf[n][k][0] = __byte_perm(v.x, v.y, 0x5410);
+              qf[n][k][1] = __byte_perm(v.x, v.y, 0x7632);
             } else {
               qf[n][k][0] = *reinterpret_cast<const uint32_t*>(p + 4 * t);
               qf[n][k][1] = *reinterpret_cast<const uint32_t*>(p + 16 + 4 * t);
@@ -359,27 +369,26 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const int left = b.left - 16 * warp;  // keys of this slice that exist
       if (left > 0 && ((b.slices >> warp) & 1u)) {
         const uint32_t kb = smem_addr(smem + s * SM::SLOT) + slice, vb = kb + SM::TILE;
-        float sc[NT][4];
+        float sc[NT][4], sd[NT][4];  // two chains of products
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] = 0.f;
+          for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
         if (I8) {
           // one ldmatrix covers 32 elements: a lane gets elements 4t .. 4t+3 of
-          // row g (and g + 8) of each 16; the first two stand as the step's
-          // columns 2t, 2t+1, the others as 2t+8, 2t+9, in K and Q alike
+          // row g (and g + 8) of each 16; the even ones stand as the step's
+          // columns 2t, 2t+1, the odd ones as 2t+8, 2t+9, in K and Q alike
 #pragma unroll
           for (int k = 0; k < KS; k += 2) {
             uint32_t r[4];
             ldsm_x4(line(kb, lane & 15, k + (lane >> 4)), r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = codes_to_bf16(__byte_perm(r[2 * h], 0, 0x4140));
-              const uint32_t a2 = codes_to_bf16(__byte_perm(r[2 * h], 0, 0x4342));
-              const uint32_t a1 = codes_to_bf16(__byte_perm(r[2 * h + 1], 0, 0x4140));
-              const uint32_t a3 = codes_to_bf16(__byte_perm(r[2 * h + 1], 0, 0x4342));
+              const uint32_t a0 = codes_to_bf16(r[2 * h]), a2 = codes_to_bf16(r[2 * h] >> 8);
+              const uint32_t a1 = codes_to_bf16(r[2 * h + 1]), a3 = codes_to_bf16(r[2 * h + 1] >> 8);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_16x8x16(sc[n], a0, a1, a2, a3, qf[n][k + h][0], qf[n][k + h][1]);
+              for (int n = 0; n < NT; ++n)
+                mma_16x8x16(h ? sd[n] : sc[n], a0, a1, a2, a3, qf[n][k + h][0], qf[n][k + h][1]);
             }
           }
         } else {
@@ -388,7 +397,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             uint32_t r[4];
             ldsm_x4(line(kb, lane & 15, 2 * k + (lane >> 4)), r);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16x8x16(sc[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
+            for (int n = 0; n < NT; ++n) mma_16x8x16(k & 1 ? sd[n] : sc[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
           }
         }
         // rows g and g + 8: keys; columns 2t and 2t + 1: heads
@@ -405,7 +414,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            sc[n][e] *= ks[e >> 1];
+            sc[n][e] = (sc[n][e] + sd[n][e]) * ks[e >> 1];
             if (g + 8 * (e >> 1) >= left) sc[n][e] = -INFINITY;
             high |= sc[n][e] > m[n][e & 1] + 8.f;
           }
@@ -452,10 +461,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             ldsm_x4_t(line(vb, lane & 15, k + (lane >> 4)), r);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = codes_to_bf16(__byte_perm(r[2 * h], 0, 0x4240));
-              const uint32_t a1 = codes_to_bf16(__byte_perm(r[2 * h], 0, 0x4341));
-              const uint32_t a2 = codes_to_bf16(__byte_perm(r[2 * h + 1], 0, 0x4240));
-              const uint32_t a3 = codes_to_bf16(__byte_perm(r[2 * h + 1], 0, 0x4341));
+              const uint32_t a0 = codes_to_bf16(r[2 * h]), a1 = codes_to_bf16(r[2 * h] >> 8);
+              const uint32_t a2 = codes_to_bf16(r[2 * h + 1]), a3 = codes_to_bf16(r[2 * h + 1] >> 8);
 #pragma unroll
               for (int n = 0; n < NT; ++n) mma_16x8x16(acc[n][k + h], a0, a1, a2, a3, pb[n][0], pb[n][1]);
             }

@@ -37,7 +37,7 @@ def norm_rotate(x, weight, table, positions, eps):
     return y, 20 * U * np.concatenate([size, size, np.abs(x[..., 2 * half:])], -1)
 
 
-def attention(q, k, v, scale, visible):
+def attention(q, k, v, scale, visible, q_bits16=False):
     """One head's rows: q [n, D], k, v [m, D], visible bool [n, m] ->
     (o [n, D], tol [n, D]).
 
@@ -49,7 +49,10 @@ def attention(q, k, v, scale, visible):
       in the sum;
     * exp2: 2^-12 relative; the probability's rounding: 2^-8;
     * sums of m terms in fp32: m unit roundoffs;
-    * the result's rounding: 2^-8 of the result.
+    * the result's rounding: 2^-8 of the result;
+    * q_bits16 (int8 caches): each query element off by half a step of a
+      16-bit grid, max|q| / 32512 / 2, which moves a score by scale * sum |k|
+      times that.
     """
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     n, d = q.shape
@@ -64,6 +67,8 @@ def attention(q, k, v, scale, visible):
         p /= p.sum()
         o[i] = p @ v[see]
         ds = 2 * d * U * scale * (np.abs(k[see]) @ np.abs(q[i])).max()
+        if q_bits16:
+            ds += scale * np.abs(q[i]).max() / 65024 * np.abs(k[see]).sum(1).max()
         rel = BF16 + 2.0 ** -12 + 2 * ds + m * U
         tol[i] = (1 + BF16) * rel * (p @ np.abs(v[see])) + BF16 * np.abs(o[i])
     return o, tol
@@ -102,5 +107,5 @@ def paged_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale):
         v = cache_rows(v_cache, v_scale, table[b], n)
         for h in range(q.shape[1]):
             o[b, h], tol[b, h] = (x[0] for x in attention(q[b, h][None], k[:, h // group], v[:, h // group], scale,
-                                                          np.ones((1, n), bool)))
+                                                          np.ones((1, n), bool), k_scale is not None))
     return o, tol

@@ -19,7 +19,7 @@
 // head rows, APPEND_UNROLL row groups in flight at a time.
 #pragma once
 
-#include "ptx.cuh"
+#include "attn_row.cuh"
 
 namespace convrot {
 
@@ -42,12 +42,6 @@ struct AppendArgs {
 
 constexpr int APPEND_WARPS = 4;
 constexpr int APPEND_UNROLL = 4;
-
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 
 __device__ __forceinline__ void bf16x8_to_f32(const uint4& u, float* f) {
   const uint32_t w[4] = {u.x, u.y, u.z, u.w};

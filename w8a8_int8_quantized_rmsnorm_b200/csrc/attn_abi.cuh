@@ -297,12 +297,18 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   // no more CTAs than blocks there can be
   const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + DECODE_KEYS - 1) / DECODE_KEYS);
   const int64_t blocks = most * seqs * kv_heads * a.chunks;
-  const bool i8 = k_scale != nullptr, wide = a.chunk_heads > 8;
+  const bool i8 = k_scale != nullptr;
+  const int h = a.chunk_heads;
   cudaStream_t st = as_cuda(stream);
-#define CONVROT_DECODE(D)                                                                                     \
-  (i8 ? (wide ? run_decode<D, true, 16>(a, k_cache, v_cache, blocks, st) : run_decode<D, true, 8>(a, k_cache, v_cache, blocks, st)) \
-      : (wide ? run_decode<D, false, 16>(a, k_cache, v_cache, blocks, st) : run_decode<D, false, 8>(a, k_cache, v_cache, blocks, st)))
-  return head_dim == 128 ? CONVROT_DECODE(128) : CONVROT_DECODE(64);
+#define CONVROT_DECODE(D, I8, NQ) run_decode<D, I8, NQ>(a, k_cache, v_cache, blocks, st)
+  // heads of a unit: one 8-column tile takes eight (bf16) or four (int8, in
+  // two columns each); fewer tiles leave registers for more CTAs per SM
+  if (head_dim == 128) {
+    if (i8) return h > 8 ? CONVROT_DECODE(128, true, 16) : h > 4 ? CONVROT_DECODE(128, true, 8) : CONVROT_DECODE(128, true, 4);
+    return h > 8 ? CONVROT_DECODE(128, false, 16) : CONVROT_DECODE(128, false, 8);
+  }
+  if (i8) return h > 8 ? CONVROT_DECODE(64, true, 16) : h > 4 ? CONVROT_DECODE(64, true, 8) : CONVROT_DECODE(64, true, 4);
+  return h > 8 ? CONVROT_DECODE(64, false, 16) : CONVROT_DECODE(64, false, 8);
 #undef CONVROT_DECODE
 }
 

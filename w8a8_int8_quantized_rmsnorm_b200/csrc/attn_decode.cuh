@@ -16,13 +16,21 @@
 // compute, each 16 keys of a block, on warp-level matrix instructions with the
 // keys as rows and the heads as columns: S^T = K Q^T and O^T += V^T P^T, so a
 // group of four or eight heads fills the 8-column operand and every score
-// stays with the lane that made it.  16 keys x 8 heads are 2 * D / 16 products
-// against 4 D (bf16) bytes a key: the tensor pipe idles, memory bounds.
+// stays with the lane that made it.
 //
 // Each warp keeps a reference maximum per head, raised (with O and l) only
 // when a score lies more than 2^8 above it, and fp32 sums; probabilities are
-// rounded to bf16 for the product with V.  int8 codes become bf16 exactly in
-// registers; a key's scale multiplies its score, a value's its probability.
+// rounded to bf16 for the product with V.
+//
+// int8 caches.  Turning codes into bf16 costs 7 instructions per 4 codes, more
+// than the stream leaves time for (both sides converted: 288 us for 128
+// contexts of 1 .. 8192 keys).  So the scores are integer products: a head's
+// query becomes 16-bit fixed point, q = s (256 hi + lo) with s = max|q| / 32512,
+// and hi and lo are two columns of one s8 x s8 -> s32 product with the codes
+// as they are.  The sums are exact; the query is off by at most 2^-16 of its
+// largest element, which moves a score by scale 2^-16 max|q| sum|k| at most,
+// less than the rounding of the probabilities moves the result.  Values become
+// bf16 exactly.  A key's scale multiplies its score, a value's its probability.
 //
 // Rows past a sequence's end are never used: their scores are replaced, their
 // values' registers cleared, pages behind the last one not fetched.
@@ -72,7 +80,7 @@ struct DecodeSmem {
   static constexpr int ESZ = I8 ? 1 : 2;
   // CTAs per SM: two keep enough bf16 rows in flight (64 contexts of 1 .. 8192
   // keys: 0.98 of HBM); int8 rows need more warps, for the conversions
-  static constexpr int CTAS = I8 && NQ == 8 ? 3 : 2;
+  static constexpr int CTAS = I8 && NQ <= 8 ? 3 : 2;
   static constexpr int TILE = DECODE_KEYS * D * ESZ;
   static constexpr int SLOT = 2 * TILE;                            // K, V
   static constexpr int SIDE = NQ * D * 2 + 2 * DECODE_KEYS * 4;    // Q rows, scales
@@ -107,6 +115,13 @@ __device__ __forceinline__ void mma_16x8x16(float (&d)[4], uint32_t a0, uint32_t
       "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
       : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// d += a (16 x 32, rows) * b (32 x 8, columns), int8 in, int32 out
+__device__ __forceinline__ void mma_16x8x32(int (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 // Two int8 codes, bytes 0 and 2 of x, as bf16, exactly:
 // (128 + low 7 bits) - (128 or, with the sign bit, 256).
@@ -145,7 +160,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   using SM = DecodeSmem<D, I8, NQ>;
   constexpr int ROWB = D * SM::ESZ >= 128 ? 128 : 64;  // bytes of a swizzled line
   constexpr int HALVES = D * SM::ESZ / ROWB;
-  constexpr int NT = NQ / 8;                           // 8-head column tiles
+  constexpr int HL = NQ / 4;                           // heads of a lane
+  constexpr int NT = (HL + 1) / 2;                     // 8-column tiles of P and O
   constexpr int KS = D / 16;                           // 16-element steps
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
@@ -179,19 +195,30 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   const int units = a.kv_heads * a.chunks;
   if (warp == 4) {
     // -------------------------------------------------------- fetch
-    // this CTA's stretch [at, end) of the line of blocks
+    // this CTA's stretch [begin, end) of the line of blocks
     int64_t total = 0;
-    for (int b0 = 0; b0 < a.seqs; b0 += 32) {
-      int n = b0 + lane < a.seqs ? decode_blocks(decode_length(a, b0 + lane)) : 0;
-      total += __reduce_add_sync(0xFFFFFFFFu, n);
+    for (int b0 = lane; b0 < a.seqs; b0 += 128) {
+      int n = 0;
+#pragma unroll
+      for (int x = 0; x < 4; ++x)  // four loads in flight
+        if (b0 + 32 * x < a.seqs) n += decode_blocks(decode_length(a, b0 + 32 * x));
+      total += n;
     }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     total *= units;
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x;
-    int64_t at = begin;
-    const int64_t end = min(total, at + per);
-    int seq = 0, len = 0, nb = 1, unit = 0, j = 0;
-    int64_t start = 0;                       // line index of the sequence's first block
-    if (at < end) {
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x, end = min(total, begin + per);
+
+    // A batch: consecutive blocks of one (sequence, unit), as many as a warp's
+    // lanes can hold the pages of, so that the block table's latency is paid
+    // once per batch and behind the one before.
+    const int boxes = DECODE_KEYS / a.box_rows, most = 32 / boxes;
+    const unsigned page_size = a.page_size;
+    struct Batch {
+      int64_t at, start;  // line index of the batch, and of the sequence's first block
+      int seq, unit, len, nb, j, n;
+    } cur = {begin, 0, 0, 0, 0, 1, 0, 0}, next;
+    if (begin < end) {
       for (int b0 = 0;; b0 += 32) {
         const int ln = b0 + lane < a.seqs ? decode_length(a, b0 + lane) : 0;
         const int n = b0 + lane < a.seqs ? decode_blocks(ln) : 0;
@@ -201,107 +228,111 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
           if (lane >= o) sum += up;
         }
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, start + static_cast<int64_t>(sum) * units > at);
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, cur.start + static_cast<int64_t>(sum) * units > begin);
         if (hit) {
           const int l = __ffs(hit) - 1;
-          seq = b0 + l;
-          len = __shfl_sync(0xFFFFFFFFu, ln, l);
-          nb = decode_blocks(len);
-          start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, l) - nb) * units;
+          cur.seq = b0 + l;
+          cur.len = __shfl_sync(0xFFFFFFFFu, ln, l);
+          cur.nb = decode_blocks(cur.len);
+          cur.start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, l) - cur.nb) * units;
           break;
         }
-        start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, 31)) * units;
+        cur.start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, 31)) * units;
       }
-      unit = static_cast<int>((at - start) / nb);
-      j = static_cast<int>((at - start) - static_cast<int64_t>(unit) * nb);
+      cur.unit = static_cast<int>((begin - cur.start) / cur.nb);
+      cur.j = static_cast<int>((begin - cur.start) - static_cast<int64_t>(cur.unit) * cur.nb);
     }
-    const int boxes = DECODE_KEYS / a.box_rows;
-    const unsigned page_size = a.page_size;
-    // page of this lane's box of a block; -1: not there
-    auto entry = [&](int b, int blk, int n) -> int {
-      const unsigned key = static_cast<unsigned>(blk) * DECODE_KEYS + lane * a.box_rows;
-      return lane < boxes && key < static_cast<unsigned>(n) ? a.table[b * a.table_stride + key / page_size] : -1;
+    auto size = [&](const Batch& b) {
+      return static_cast<int>(min(static_cast<int64_t>(min(most, b.nb - b.j)), end - b.at));
+    };
+    // page of this lane's box of the batch; -1: not there
+    auto pages_of = [&](const Batch& b) -> int {
+      const unsigned key = static_cast<unsigned>(b.j) * DECODE_KEYS + lane * a.box_rows;
+      if (lane >= b.n * boxes || key >= static_cast<unsigned>(b.len)) return -1;
+      return a.table[b.seq * a.table_stride + key / page_size];
     };
     bool ok = true;
     uint32_t it = 0, s = 0, phase = 1;  // slot and the parity its last emptying has
-    int page = at < end ? entry(seq, j, len) : -1;
+    cur.n = size(cur);
+    int page = begin < end ? pages_of(cur) : -1;
     const int group = a.q_heads / a.kv_heads;
-    int kvh = unit / a.chunks, chunk = unit - kvh * a.chunks;
-    int next_len = seq + 1 < a.seqs ? decode_length(a, seq + 1) : 0;
-    while (at < end && ok) {
-      // where the line goes on, and that block's pages
-      int seq2 = seq, len2 = len, nb2 = nb, unit2 = unit, j2 = j + 1;
-      int64_t start2 = start;
-      if (j2 == nb) {
-        j2 = 0;
-        if (++unit2 == units) {
-          unit2 = 0;
-          ++seq2;
-          start2 += static_cast<int64_t>(nb) * units;
-          len2 = next_len;
-          nb2 = decode_blocks(len2);
+    int next_len = cur.seq + 1 < a.seqs ? decode_length(a, cur.seq + 1) : 0;
+    while (cur.at < end && ok) {
+      // where the line goes on, and that batch's pages
+      next = cur;
+      next.at += cur.n;
+      next.j += cur.n;
+      if (next.j == cur.nb) {
+        next.j = 0;
+        if (++next.unit == units) {
+          next.unit = 0;
+          ++next.seq;
+          next.start += static_cast<int64_t>(cur.nb) * units;
+          next.len = next_len;
+          next.nb = decode_blocks(next_len);
         }
       }
-      const bool more = at + 1 < end;
-      const int page2 = more ? entry(seq2, j2, len2) : -1;
-      if (seq2 != seq) next_len = seq2 + 1 < a.seqs ? decode_length(a, seq2 + 1) : 0;
-
-      ok = mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
-      if (!ok) break;
+      int page2 = -1;
+      if (next.at < end) {
+        next.n = size(next);
+        const bool same = next.seq == cur.seq && next.j == cur.j && next.n <= cur.n;  // another head, the same pages
+        page2 = same ? page : pages_of(next);
+        if (next.seq != cur.seq) next_len = next.seq + 1 < a.seqs ? decode_length(a, next.seq + 1) : 0;
+      }
+      const int kvh = cur.unit / a.chunks, chunk = cur.unit - kvh * a.chunks;
       const int qh = min(heads, group - chunk * heads);
-      const unsigned key = static_cast<unsigned>(j) * DECODE_KEYS + lane * a.box_rows;  // of this lane's box
-      const bool wanted = lane < boxes && key < static_cast<unsigned>(len);
-      const bool there = wanted && page >= 0 && page < a.pages;
-      if (wanted && !there) report_error(ERR_BAD_ARGUMENT);
-      const unsigned mask = __ballot_sync(0xFFFFFFFFu, there);
-      const bool first = at == begin || j == 0;
-      const bool last = j + 1 == nb || !more;
-      if (lane == 0) {
-        DecodeBlock m;
-        m.seq = seq;
-        m.unit = unit;
-        m.left = len - j * DECODE_KEYS;
-        m.slices = 0;
-        for (int x = 0; x < 4; ++x) m.slices |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
-        m.first = first;
-        m.last = last;
-        m.owner = blockIdx.x;
-        m.n_parts = 1;
-        const int64_t item = start + static_cast<int64_t>(unit) * nb;
-        if (last && (item < begin || item + nb > end)) {  // twice per CTA at most: its two ends
-          m.owner = static_cast<int>(item / per);
-          m.n_parts = static_cast<int>((item + nb - 1) / per) - m.owner + 1;
+      const int64_t item = cur.start + static_cast<int64_t>(cur.unit) * cur.nb;
+      for (int i = 0; i < cur.n; ++i) {
+        ok = mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
+        if (!ok) break;
+        const int j = cur.j + i;
+        const int mine = __shfl_sync(0xFFFFFFFFu, page, (i * boxes + lane) & 31);
+        const unsigned key = static_cast<unsigned>(j) * DECODE_KEYS + lane * a.box_rows;  // of this lane's box
+        const bool wanted = lane < boxes && key < static_cast<unsigned>(cur.len);
+        const bool there = wanted && mine >= 0 && mine < a.pages;
+        if (wanted && !there) report_error(ERR_BAD_ARGUMENT);
+        const unsigned mask = __ballot_sync(0xFFFFFFFFu, there);
+        const bool first = cur.at + i == begin || j == 0;
+        const bool last = cur.at + i + 1 == end || j + 1 == cur.nb;
+        if (lane == 0) {
+          DecodeBlock m;
+          m.seq = cur.seq;
+          m.unit = cur.unit;
+          m.left = cur.len - j * DECODE_KEYS;
+          m.slices = 0;
+          for (int x = 0; x < 4; ++x) m.slices |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
+          m.first = first;
+          m.last = last;
+          m.owner = blockIdx.x;
+          m.n_parts = 1;
+          if (last && (item < begin || item + cur.nb > end)) {  // twice per CTA at most: its two ends
+            m.owner = static_cast<int>(item / per);
+            m.n_parts = static_cast<int>((item + cur.nb - 1) / per) - m.owner + 1;
+          }
+          meta[s] = m;
+          const uint32_t bytes = __popc(mask) * a.box_rows * (2 * D * SM::ESZ + (I8 ? 8 : 0)) + (first ? qh * D * 2 : 0);
+          mbar_arrive_expect_tx(&full[s], bytes);
+          if (first)
+            bulk_load_1d(side + s * SM::SIDE,
+                         a.q + cur.seq * a.q_stride + (static_cast<int64_t>(kvh) * group + chunk * heads) * D, qh * D * 2,
+                         &full[s]);
         }
-        meta[s] = m;
-        const uint32_t bytes = __popc(mask) * a.box_rows * (2 * D * SM::ESZ + (I8 ? 8 : 0)) + (first ? qh * D * 2 : 0);
-        mbar_arrive_expect_tx(&full[s], bytes);
-        if (first)
-          bulk_load_1d(side + s * SM::SIDE,
-                       a.q + seq * a.q_stride + (static_cast<int64_t>(kvh) * group + chunk * heads) * D, qh * D * 2,
-                       &full[s]);
-      }
-      __syncwarp();
-      if (there) {
-        const int64_t row = (static_cast<int64_t>(page) * a.kv_heads + kvh) * page_size + key % page_size;
-        uint8_t* dst = smem + s * SM::SLOT + lane * a.box_rows * D * SM::ESZ;
-        tma_load_3d(dst, &tm_k, &full[s], 0, static_cast<int>(row), 0);
-        tma_load_3d(dst + SM::TILE, &tm_v, &full[s], 0, static_cast<int>(row), 0);
-        if (I8) {
-          float* sc = reinterpret_cast<float*>(side + s * SM::SIDE + NQ * D * 2) + lane * a.box_rows;
-          bulk_load_1d(sc, a.k_scale + row, a.box_rows * 4, &full[s]);
-          bulk_load_1d(sc + DECODE_KEYS, a.v_scale + row, a.box_rows * 4, &full[s]);
+        __syncwarp();
+        if (there) {
+          const int64_t row = (static_cast<int64_t>(mine) * a.kv_heads + kvh) * page_size + key % page_size;
+          uint8_t* dst = smem + s * SM::SLOT + lane * a.box_rows * D * SM::ESZ;
+          tma_load_3d(dst, &tm_k, &full[s], 0, static_cast<int>(row), 0);
+          tma_load_3d(dst + SM::TILE, &tm_v, &full[s], 0, static_cast<int>(row), 0);
+          if (I8) {
+            float* sc = reinterpret_cast<float*>(side + s * SM::SIDE + NQ * D * 2) + lane * a.box_rows;
+            bulk_load_1d(sc, a.k_scale + row, a.box_rows * 4, &full[s]);
+            bulk_load_1d(sc + DECODE_KEYS, a.v_scale + row, a.box_rows * 4, &full[s]);
+          }
         }
+        ++it;
+        if (++s == static_cast<uint32_t>(S)) s = 0, phase ^= 1u;
       }
-      ++it;
-      if (++s == static_cast<uint32_t>(S)) s = 0, phase ^= 1u;
-      ++at;
-      if (unit2 != unit) kvh = unit2 / a.chunks, chunk = unit2 - kvh * a.chunks;
-      seq = seq2;
-      len = len2;
-      nb = nb2;
-      unit = unit2;
-      j = j2;
-      start = start2;
+      cur = next;
       page = page2;
     }
     ok = ok && mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
@@ -318,9 +349,13 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   } else {
     // -------------------------------------------------------- compute
     const int g = lane >> 2, t = lane & 3;
-    uint32_t qf[NT][KS][2];
+    // A lane's scores: keys g and g + 8, heads head(0 .. HL-1); head(x) is
+    // column 2 t + (x & 1) of tile x / 2 in P and O.
+    auto head = [&](int x) { return I8 ? 4 * x + t : (x / 2) * 8 + 2 * t + (x & 1); };
+    uint32_t qf[I8 ? HL : NT][KS][I8 ? 1 : 2];  // queries as the second operand
+    float qs[HL];                               // int8: scale of the head's query
     float acc[NT][KS][4];
-    float m[NT][2], l[NT][2];
+    float m[HL], l[HL];
     uint32_t met = 0, parity = 0;
     // bounded rendezvous of the four compute warps
     auto rendezvous = [&]() -> bool {
@@ -345,113 +380,133 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const DecodeBlock b = meta[s];
       if (b.seq < 0) break;
       if (b.first) {
-        const uint8_t* qs = side + s * SM::SIDE;
+        const uint8_t* rows = side + s * SM::SIDE;
+        if (I8) {
+          // columns 2h and 2h + 1 of a tile: hi and lo of head h; this lane's is column g
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
+          for (int x = 0; x < HL; ++x) {
+            const uint8_t* p = rows + (4 * x + (g >> 1)) * D * 2 + 8 * t;
+            float v[KS][4], top = 0.f;
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            const uint8_t* p = qs + ((n * 8 + g) * D + k * 16) * 2;
-            if (I8) {  // elements 4t .. 4t+3 of the step: see the keys' bytes below
-              const uint2 v = *reinterpret_cast<const uint2*>(p + 8 * t);
-              qf[n][k][0] = __byte_perm(v.x, v.y, 0x5410);
-              qf[n][k][1] = __byte_perm(v.x, v.y, 0x7632);
-            } else {
-              qf[n][k][0] = *reinterpret_cast<const uint32_t*>(p + 4 * t);
-              qf[n][k][1] = *reinterpret_cast<const uint32_t*>(p + 16 + 4 * t);
+            for (int k = 0; k < KS; ++k) {
+              const uint2 w = *reinterpret_cast<const uint2*>(p + 32 * k);  // elements 16k + 4t ..
+              v[k][0] = __uint_as_float(w.x << 16), v[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
+              v[k][2] = __uint_as_float(w.y << 16), v[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) top = max_nan(top, fabsf(v[k][e]));
             }
+            top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // scaled up first where 1 / top would overflow
+            const float up = top < 1e-30f ? 0x1p64f : 1.f;
+            const float inv = top > 0.f ? 32512.f / (top * up) : 0.f;
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              qf[x][k][0] = 0;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int q = max(-32512, min(32512, __float2int_rn(v[k][e] * up * inv)));
+                const int hi = (q + 128) >> 8, lo = q - hi * 256;
+                qf[x][k][0] |= (static_cast<uint32_t>(g & 1 ? lo : hi) & 0xFFu) << (8 * e);
+              }
+            }
+            // the scores' scale belongs to head 4x + t, held by lanes g = 2t, 2t + 1
+            qs[x] = __shfl_sync(0xFFFFFFFFu, top, 8 * t) * (1.f / 32512.f);
+          }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int k = 0; k < KS; ++k) {
+              const uint8_t* p = rows + ((n * 8 + g) * D + k * 16) * 2;
+              qf[n][k][0] = *reinterpret_cast<const uint32_t*>(p + 4 * t);
+              qf[n][k][I8 ? 0 : 1] = *reinterpret_cast<const uint32_t*>(p + 16 + 4 * t);
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int k = 0; k < KS; ++k)
 #pragma unroll
             for (int e = 0; e < 4; ++e) acc[n][k][e] = 0.f;
-          }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) m[n][e] = -INFINITY, l[n][e] = 0.f;
-        }
+        for (int x = 0; x < HL; ++x) m[x] = -INFINITY, l[x] = 0.f;
       }
       const int left = b.left - 16 * warp;  // keys of this slice that exist
       if (left > 0 && ((b.slices >> warp) & 1u)) {
         const uint32_t kb = smem_addr(smem + s * SM::SLOT) + slice, vb = kb + SM::TILE;
-        float sc[NT][4], sd[NT][4];  // two chains of products
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sc[n][e] = sd[n][e] = 0.f;
+        float sc[HL][2];  // scores of keys g and g + 8, times log2(e)
+        float vs[2] = {1.f, 1.f};
         if (I8) {
-          // one ldmatrix covers 32 elements: a lane gets elements 4t .. 4t+3 of
-          // row g (and g + 8) of each 16; the even ones stand as the step's
-          // columns 2t, 2t+1, the odd ones as 2t+8, 2t+9, in K and Q alike
+          int c[HL][4] = {};
 #pragma unroll
           for (int k = 0; k < KS; k += 2) {
             uint32_t r[4];
             ldsm_x4(line(kb, lane & 15, k + (lane >> 4)), r);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = codes_to_bf16(r[2 * h]), a2 = codes_to_bf16(r[2 * h] >> 8);
-              const uint32_t a1 = codes_to_bf16(r[2 * h + 1]), a3 = codes_to_bf16(r[2 * h + 1] >> 8);
-#pragma unroll
-              for (int n = 0; n < NT; ++n)
-                mma_16x8x16(h ? sd[n] : sc[n], a0, a1, a2, a3, qf[n][k + h][0], qf[n][k + h][1]);
-            }
+            for (int x = 0; x < HL; ++x) mma_16x8x32(c[I8 ? x : 0], r, qf[I8 ? x : 0][k][0], qf[I8 ? x : 0][k + 1][0]);
           }
+          const float* scales = reinterpret_cast<const float*>(side + s * SM::SIDE + NQ * D * 2) + 16 * warp + g;
+          const float ks[2] = {scales[0] * a.scale_log2, scales[8] * a.scale_log2};
+          vs[0] = g < left ? scales[DECODE_KEYS] : 0.f;
+          vs[1] = g + 8 < left ? scales[DECODE_KEYS + 8] : 0.f;
+#pragma unroll
+          for (int x = 0; x < HL; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)  // |256 hi + lo| < 2^30
+              sc[x][r] = static_cast<float>(c[x][2 * r] * 256 + c[x][2 * r + 1]) * qs[x] * ks[r];
         } else {
+          float c[NT][4] = {}, d[NT][4] = {};  // two chains of products
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t r[4];
             ldsm_x4(line(kb, lane & 15, 2 * k + (lane >> 4)), r);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16x8x16(k & 1 ? sd[n] : sc[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
+            for (int n = 0; n < NT; ++n)
+              mma_16x8x16(k & 1 ? d[n] : c[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][I8 ? 0 : 1]);
           }
-        }
-        // rows g and g + 8: keys; columns 2t and 2t + 1: heads
-        float ks[2] = {a.scale_log2, a.scale_log2}, vs[2] = {1.f, 1.f};
-        if (I8) {
-          const float* scales = reinterpret_cast<const float*>(side + s * SM::SIDE + NQ * D * 2) + 16 * warp + g;
-          ks[0] *= scales[0];
-          ks[1] *= scales[8];
-          vs[0] = scales[DECODE_KEYS];
-          vs[1] = scales[DECODE_KEYS + 8];
+#pragma unroll
+          for (int x = 0; x < HL; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) sc[x][r] = (c[x / 2][2 * r + (x & 1)] + d[x / 2][2 * r + (x & 1)]) * a.scale_log2;
         }
         bool high = false;
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int x = 0; x < HL; ++x)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            sc[n][e] = (sc[n][e] + sd[n][e]) * ks[e >> 1];
-            if (g + 8 * (e >> 1) >= left) sc[n][e] = -INFINITY;
-            high |= sc[n][e] > m[n][e & 1] + 8.f;
+          for (int r = 0; r < 2; ++r) {
+            if (g + 8 * r >= left) sc[x][r] = -INFINITY;
+            high |= sc[x][r] > m[x] + 8.f;
           }
         if (__any_sync(0xFFFFFFFFu, high)) {
 #pragma unroll
-          for (int n = 0; n < NT; ++n)
+          for (int x = 0; x < HL; ++x) {
+            float top = fmaxf(m[x], fmaxf(sc[x][0], sc[x][1]));
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              float top = fmaxf(m[n][e], fmaxf(sc[n][e], sc[n][e + 2]));
+            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            const float f = top > m[x] ? ex2_approx(m[x] - top) : 1.f;
+            m[x] = top;
+            l[x] *= f;
 #pragma unroll
-              for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-              const float f = top > m[n][e] ? ex2_approx(m[n][e] - top) : 1.f;
-              m[n][e] = top;
-              l[n][e] *= f;
+            for (int k = 0; k < KS; ++k) acc[x / 2][k][x & 1] *= f, acc[x / 2][k][(x & 1) + 2] *= f;
+          }
+        }
+        float p[2 * NT][2] = {};
 #pragma unroll
-              for (int k = 0; k < KS; ++k) acc[n][k][e] *= f, acc[n][k][e + 2] *= f;
-            }
+        for (int x = 0; x < HL; ++x) {
+          const float base = m[x] == -INFINITY ? 0.f : m[x];
+#pragma unroll
+          for (int r = 0; r < 2; ++r) {
+            p[x][r] = ex2_approx(sc[x][r] - base);
+            l[x] += p[x][r];
+            if (I8) p[x][r] *= vs[r];
+          }
         }
         uint32_t pb[NT][2];
-        if (I8 && left < 16) {
-          if (g >= left) vs[0] = 0.f;
-          if (g + 8 >= left) vs[1] = 0.f;
-        }
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-          float p[4];
+        for (int n = 0; n < NT; ++n)  // [key][head] to [head][key]: the second operand of the next product
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float base = m[n][e & 1] == -INFINITY ? 0.f : m[n][e & 1];
-            p[e] = ex2_approx(sc[n][e] - base);
-            l[n][e & 1] += p[e];
-            if (I8) p[e] *= vs[e >> 1];
-          }
-          // [key][head] to [head][key]: the second operand of the next product
-          pb[n][0] = transpose8x8(bf16x2_of(p[0], p[1]));
-          pb[n][1] = transpose8x8(bf16x2_of(p[2], p[3]));
-        }
+          for (int r = 0; r < 2; ++r) pb[n][r] = transpose8x8(bf16x2_of(p[2 * n][r], p[2 * n + 1][r]));
         if (I8) {
           // a lane gets, for keys 2t and 2t + 1, elements 2g and 2g + 1: the
           // even ones stand as rows g, the odd ones as rows g + 8
@@ -493,39 +548,35 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       float* all = stat_all + parity * NQ * 2;
       parity ^= 1u;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int x = 0; x < HL; ++x) {
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) l[n][e] += __shfl_xor_sync(0xFFFFFFFFu, l[n][e], o);
-          if (g == 0) {
-            st[(warp * NQ + n * 8 + 2 * t + e) * 2] = m[n][e];
-            st[(warp * NQ + n * 8 + 2 * t + e) * 2 + 1] = l[n][e];
-          }
+        for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], o);
+        if (g == 0) {
+          st[(warp * NQ + head(x)) * 2] = m[x];
+          st[(warp * NQ + head(x)) * 2 + 1] = l[x];
         }
+      }
       if (!rendezvous()) break;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int x = 0; x < HL; ++x) {
+        const int h = head(x);
+        float top = -INFINITY, sum = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int h = n * 8 + 2 * t + e;
-          float top = -INFINITY, sum = 0.f;
+        for (int y = 0; y < 4; ++y) top = fmaxf(top, st[(y * NQ + h) * 2]);
+        const float base = top == -INFINITY ? 0.f : top;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top = fmaxf(top, st[(x * NQ + h) * 2]);
-          const float base = top == -INFINITY ? 0.f : top;
+        for (int y = 0; y < 4; ++y) sum += st[(y * NQ + h) * 2 + 1] * ex2_approx(st[(y * NQ + h) * 2] - base);
+        if (warp == 0 && g == 0) all[h * 2] = top, all[h * 2 + 1] = sum;
+        const float f = ex2_approx(m[x] - base);
+        if (h < heads) {
+          float* o = join + (warp * heads + h) * SM::PAD;
 #pragma unroll
-          for (int x = 0; x < 4; ++x) sum += st[(x * NQ + h) * 2 + 1] * ex2_approx(st[(x * NQ + h) * 2] - base);
-          if (warp == 0 && g == 0) all[h * 2] = top, all[h * 2 + 1] = sum;
-          const float f = ex2_approx(m[n][e] - base);
-          if (h < heads) {
-            float* o = join + (warp * heads + h) * SM::PAD;
-#pragma unroll
-            for (int k = 0; k < KS; ++k) {
-              o[16 * k + (I8 ? 2 * g : g)] = acc[n][k][e] * f;
-              o[16 * k + (I8 ? 2 * g + 1 : g + 8)] = acc[n][k][e + 2] * f;
-            }
+          for (int k = 0; k < KS; ++k) {
+            o[16 * k + (I8 ? 2 * g : g)] = acc[x / 2][k][x & 1] * f;
+            o[16 * k + (I8 ? 2 * g + 1 : g + 8)] = acc[x / 2][k][(x & 1) + 2] * f;
           }
         }
+      }
       if (!rendezvous()) break;
       const int kvh = b.unit / a.chunks, chunk = b.unit - kvh * a.chunks, group = a.q_heads / a.kv_heads;
       const int qh = min(heads, group - chunk * heads);

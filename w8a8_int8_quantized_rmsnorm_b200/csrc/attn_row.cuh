@@ -14,6 +14,13 @@ namespace convrot {
 
 constexpr float LOG2E = 1.4426950408889634f;
 
+// Maximum that a NaN survives.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
 __device__ __forceinline__ float bf16_at(const uint16_t* p, int i) {
   return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
 }

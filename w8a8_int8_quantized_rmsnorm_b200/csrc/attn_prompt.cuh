@@ -77,23 +77,57 @@ struct PromptUnit {
 static_assert(sizeof(PromptUnit) == 48, "unit layout");
 
 // ---------------------------------------------------------------- tcgen05 pieces
-// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16 bf16.
-__device__ __forceinline__ void mma_bf16_ss(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc,
-                                            uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
+// Shared-memory descriptors are kept as their low words (address, and for an
+// operand whose N elements are contiguous the distance of the next 64 of them)
+// beside one constant high word (8-row groups 1024 bytes apart, version 1,
+// 128-byte swizzle): the issuing thread has few registers, and a spilled
+// descriptor costs more than the product it feeds.
+constexpr uint32_t DESC_HIGH = (1024u >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t kmajor_desc(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+__device__ __forceinline__ uint32_t mnmajor_desc(uint32_t saddr, uint32_t next64) {
+  return ((saddr & 0x3FFFFu) >> 4) | ((next64 >> 4) << 16);
 }
 
-// Shared-memory descriptor of an operand whose N (or M) elements are contiguous:
-// 64-element (128-byte, swizzled) lines, one per K row; 8 K rows 1024 bytes
-// apart, the next 64 elements `next64` bytes on.
-__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t next64) {
-  return static_cast<uint64_t>((saddr & 0x3FFFFu) >> 4) | (static_cast<uint64_t>(next64 >> 4) << 16) |
-         (static_cast<uint64_t>(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16 bf16.
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T, 128 x N x 16 bf16.
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
+                                       uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "mov.b64 b, {%2, %5};\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
+      : "memory");
+}
+// r[0..15] to columns col .. col+15 of this warp's lanes.
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+      "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+        "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
 
@@ -352,21 +386,20 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + SM::RING);
       uint32_t it = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
       auto scores = [&](int w, uint32_t stage) {
-        const uint64_t qd = sw128_kmajor_desc(q_addr + w * SM::TILE), kd = sw128_kmajor_desc(ring + stage * SM::TILE);
+        const uint32_t qd = kmajor_desc(q_addr + w * SM::TILE), kd = kmajor_desc(ring + stage * SM::TILE);
 #pragma unroll
         for (int k = 0; k < D / 16; ++k) {
           // 32 bytes along a 128-byte line; the second half of the row is 16 KB on
           const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * 2;
-          mma_bf16_ss(tmem + TM_S + w * 128, qd + off, kd + off, idesc_s, k > 0);
+          mma_ss(tmem + TM_S + w * 128, qd + off, kd + off, idesc_s, k > 0);
         }
         mma_commit(&s_full[w]);
       };
       auto values = [&](int w, uint32_t stage, bool accumulate) {
-        const uint32_t base = ring + stage * SM::TILE;
+        const uint32_t vd = mnmajor_desc(ring + stage * SM::TILE, 16384);
 #pragma unroll
-        for (int k = 0; k < PROMPT_KEYS / 16; ++k)
-          mma_bf16_ts(tmem + TM_O + w * 128, tmem + TM_S + w * 128 + k * 8,
-                      sw128_mnmajor_desc(base + k * 2048, 16384), idesc_o, accumulate || k > 0);
+        for (int k = 0; k < PROMPT_KEYS / 16; ++k)  // 16 keys: 16 lines of 128 bytes
+          mma_ts(tmem + TM_O + w * 128, tmem + TM_S + w * 128 + k * 8, vd + k * (2048 >> 4), idesc_o, accumulate || k > 0);
         mma_commit(&o_done[w]);
       };
       bool ok = true;
@@ -438,10 +471,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     uint32_t s_use = 0;  // S tiles taken so far = O products awaited or not
     for (uint32_t n_info = 0;; ++n_info) {
       if (!prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 4)) break;
-      const PromptUnit u = info[n_info & 1u];
-      __syncwarp();
+      const PromptUnit& u = info[n_info & 1u];  // read where it is needed: registers are short
       if (u.n[0] < 0) break;
-      if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
+      const int n_tiles = u.n[w];
       const int i = w * a.tile_tokens + tok;  // token of the unit
       const bool valid = tok < a.tile_tokens && i < u.ntok && hd < u.nheads;
       // rows that are not stored mask nothing
@@ -449,7 +481,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const int warp_lim = __reduce_min_sync(0xFFFFFFFFu, lim);
       float m = -INFINITY, l = 0.f;
       bool ok = true;
-      for (int j = 0; j < u.n[w]; ++j, ++s_use) {
+      for (int j = 0; j < n_tiles; ++j, ++s_use) {
         ok = prompt_wait(&s_full[w], s_use & 1u, abort_flag, busy, SITE_ATTN + 4);
         if (!ok) break;
         tc_fence_after();
@@ -482,24 +514,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int x = 0; x < D / 32; ++x) {
-            uint32_t o[32];
-            tmem_ld_32x32b_x32(t_o + 32 * x, o);
+          for (int x = 0; x < D / 16; ++x) {  // (sixteen at a time: the scores stay in registers)
+            uint32_t o[16];
+            tmem_ld_x16(t_o + 16 * x, o);
             tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            tmem_st_32x32b_x32(t_o + 32 * x, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            tmem_st_x16(t_o + 16 * x, o);
           }
         }
         const float shift = m == -INFINITY ? 0.f : -m * c;
         const uint64_t c2 = pack2(c, c), shift2 = pack2(shift, shift);
         uint64_t sum2[2] = {0, 0};
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          uint32_t p[32];
+        for (int x = 0; x < 4; ++x) {
+          uint32_t p[16];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const uint32_t* in = &s[2 * x + e / 16][(2 * e) % 32];
+          for (int e = 0; e < 16; ++e) {
+            const uint32_t* in = &s[x][2 * e];
             float lo, hi;
             unpack2(fma2(pack2(__uint_as_float(in[0]), __uint_as_float(in[1])), c2, shift2), lo, hi);
             lo = ex2(lo);
@@ -507,7 +539,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             sum2[e & 1] = add2(sum2[e & 1], pack2(lo, hi));
             p[e] = cvt_bf16x2(lo, hi);
           }
-          tmem_st_32x32b_x32(t_s + 32 * x, p);
+          tmem_st_x16(t_s + 16 * x, p);
         }
         float s0, s1;
         unpack2(add2(sum2[0], sum2[1]), s0, s1);
@@ -521,7 +553,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // ---- result
       uint16_t* out = a.o + static_cast<int64_t>(u.tok0 + i) * a.o_stride + static_cast<int64_t>(u.head0 + hd) * D;
       bool bad = false;
-      if (u.n[w] > 0) {
+      if (n_tiles > 0) {
         if (!prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
         tc_fence_after();
         const float inv = lim > 0 ? 1.f / l : 0.f;
@@ -565,6 +597,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         __syncwarp();
         if (lane == 0) atomicSub(const_cast<int*>(busy), 1);
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
     }
   }
   __syncthreads();

@@ -59,6 +59,7 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   a.head_chunks = (group + 127) / 128;
   a.tile_heads = (group + a.head_chunks - 1) / a.head_chunks;
   a.tile_tokens = 128 / a.tile_heads;
+  a.wide = aligned(a.o, 32) && a.o_stride % 16 == 0;
   CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, D, a.q_stride, a.tile_heads, a.tile_tokens))
     return CONVROT_ERR_CUDA;

@@ -45,9 +45,11 @@ struct PromptArgs {
   int head_chunks;                                 // tiles side by side for one group
   float scale_log2;                                // scale * log2(e)
   int causal;
+  int wide;                                        // result rows lie on 32-byte boundaries
 };
 
 constexpr int PROMPT_KEYS = 128;     // keys per tile
+constexpr int PROMPT_POLY = 1000;       // one pair of exp2 in so many is a polynomial
 constexpr int PROMPT_THREADS = 384;  // 2 softmax warpgroups, 1 of fetch + issue
 constexpr unsigned SITE_ATTN = 9;    // wait sites SITE_ATTN .. SITE_ATTN + 5
 
@@ -131,6 +133,21 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
 }
 constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
 
+// True in one lane of a converged warp, the same one every time.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.b32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
+// 32 bytes, a whole sector: a thread stores a row of its own, and half a
+// sector at a time takes twice as many passes through the store path.
+__device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
+               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -155,10 +172,33 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
+__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
+  uint64_t r;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+  return r;
+}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
+}
+
+// 2^x for two x <= 127 on the multiply-add pipe: x = i + f with i whole and
+// |f| <= 1/2 (adding 1.5 * 2^23 + 127 rounds x to a whole number and leaves
+// i + 127 in the low bits: the exponent of 2^i), times the cubic that fits 2^f
+// with the smallest relative error on that interval (7.5e-5; found by weighted
+// least squares with reweighting), a fiftieth of the rounding to bf16 that
+// follows.  x <= -127 gives exactly 0, a NaN stays one.
+__device__ __forceinline__ uint64_t exp2_poly2(float x0, float x1) {
+  constexpr float MAGIC = 12582912.f + 127.f;
+  const uint64_t x = pack2(max_nan(x0, -127.f), max_nan(x1, -127.f));
+  const uint64_t magic = pack2(MAGIC, MAGIC), t = add2(x, magic), f = sub2(x, sub2(t, magic));
+  uint64_t p = fma2(f, pack2(0.05517169f, 0.05517169f), pack2(0.24261117f, 0.24261117f));
+  p = fma2(f, p, pack2(0.69326097f, 0.69326097f));
+  p = fma2(f, p, pack2(0.99992806f, 0.99992806f));
+  float t0, t1;
+  unpack2(t, t0, t1);
+  return mul2(p, pack2(__uint_as_float(__float_as_uint(t0) << 23), __uint_as_float(__float_as_uint(t1) << 23)));
 }
 
 __device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
@@ -189,49 +229,35 @@ __device__ __forceinline__ bool prompt_wait(uint64_t* bar, uint32_t parity, vola
 }
 
 // ---------------------------------------------------------------- units
-// Blocks of 2 * tile_tokens tokens of sequence i; 0 (and an error) if its
-// offsets leave the tensors.
-__device__ __forceinline__ int prompt_blocks(const PromptArgs& a, int i) {
-  const int q0 = a.cu_q[i], lq = a.cu_q[i + 1] - q0, k0 = a.cu_k[i], lk = a.cu_k[i + 1] - k0;
-  if (q0 < 0 || lq < 0 || q0 > a.tokens || lq > a.tokens - q0 || k0 < 0 || lk < 0 || k0 > a.kv_tokens ||
-      lk > a.kv_tokens - k0) {
-    report_error(ERR_BAD_ARGUMENT);
-    return 0;
-  }
-  return (lq + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
-}
+// Up to 32 sequences of the pack, one per lane of the fetching warp.
+struct PromptChunk {
+  int first;              // index of lane 0's sequence
+  int before;             // blocks of the sequences before it
+  int q0, lq, k0, lk;     // this lane's sequence
+  int sum;                // blocks of the chunk's sequences up to this lane's
+  int blocks;             // of this lane's: of 2 * tile_tokens tokens
+};
 
-// The whole warp looks for the sequence that holds block `block` of the pack
-// (block < total); returns its index and the block's index inside it.
-__device__ __forceinline__ int prompt_find(const PromptArgs& a, int block, int& inside) {
-  const int lane = threadIdx.x & 31;
-  int before = 0;
-  for (int i0 = 0; i0 < a.seqs; i0 += 32) {
-    int n = i0 + lane < a.seqs ? prompt_blocks(a, i0 + lane) : 0;
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += up;
+// Reads the chunk's offsets; a sequence whose offsets leave the tensors has no
+// blocks (and is reported).
+__device__ __forceinline__ void prompt_load(const PromptArgs& a, PromptChunk& c) {
+  const int lane = threadIdx.x & 31, i = c.first + lane;
+  c.q0 = c.lq = c.k0 = c.lk = c.blocks = 0;
+  if (i < a.seqs) {
+    const int q0 = a.cu_q[i], q1 = a.cu_q[i + 1], k0 = a.cu_k[i], k1 = a.cu_k[i + 1];
+    if (q0 < 0 || q1 < q0 || q1 > a.tokens || k0 < 0 || k1 < k0 || k1 > a.kv_tokens) {
+      report_error(ERR_BAD_ARGUMENT);
+    } else {
+      c.q0 = q0, c.lq = q1 - q0, c.k0 = k0, c.lk = k1 - k0;
+      c.blocks = (c.lq + 2 * a.tile_tokens - 1) / (2 * a.tile_tokens);
     }
-    const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + sum > block);
-    if (hit) {
-      const int l = __ffs(hit) - 1;
-      inside = block - before - __shfl_sync(0xFFFFFFFFu, sum - n, l);
-      return i0 + l;
-    }
-    before += __shfl_sync(0xFFFFFFFFu, sum, 31);
   }
-  inside = 0;
-  return -1;
-}
-
-__device__ __forceinline__ int prompt_total(const PromptArgs& a) {
-  int n = 0;
-  for (int i = threadIdx.x & 31; i < a.seqs; i += 32) n += prompt_blocks(a, i);
+  c.sum = c.blocks;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) n += __shfl_xor_sync(0xFFFFFFFFu, n, o);
-  return n;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int up = __shfl_up_sync(0xFFFFFFFFu, c.sum, o);
+    if (lane >= o) c.sum += up;
+  }
 }
 
 // Keys that token `i` of the unit sees.
@@ -258,7 +284,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   volatile int* busy = reinterpret_cast<volatile int*>(tmem_slot + 2);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
 
   pdl_launch_dependents();
   if (threadIdx.x == 0) {
@@ -296,10 +322,19 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   pdl_wait();
 
   if (warp >= 8) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(D == 128 ? 72 : 64));
     if (warp == 8) {
       // ------------------------------------------------------ fetch
-      const int total = prompt_total(a);
+      // All offsets are read once to count the blocks; the chunk read last, the
+      // one whose blocks come first, stays, and others follow as they come up.
+      PromptChunk c;
+      c.before = 0;
+      for (c.first = 0;; c.first += 32) {
+        prompt_load(a, c);
+        if (c.first + 32 >= a.seqs) break;
+        c.before += __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+      }
+      const int total = c.before + __shfl_sync(0xFFFFFFFFu, c.sum, 31);
       const int heads = a.kv_heads * a.head_chunks;
       const int64_t units = static_cast<int64_t>(total) * heads;
       const int group = a.q_heads / a.kv_heads;
@@ -312,18 +347,29 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         // the blocks with the most keys first, a block's heads side by side
         const int block = total - 1 - static_cast<int>(at / heads);
         const int head = static_cast<int>(at % heads);
-        int inside;
-        const int seq = prompt_find(a, block, inside);
+        while (block < c.before) {
+          c.first -= 32;
+          prompt_load(a, c);
+          c.before -= __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+        }
+        for (int n = __shfl_sync(0xFFFFFFFFu, c.sum, 31); block >= c.before + n;) {
+          c.before += n;
+          c.first += 32;
+          prompt_load(a, c);
+          n = __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+        }
+        const int l = __ffs(__ballot_sync(0xFFFFFFFFu, c.before + c.sum > block)) - 1;
+        const int first = (block - c.before - __shfl_sync(0xFFFFFFFFu, c.sum - c.blocks, l)) * 2 * a.tile_tokens;
+        const int lq = __shfl_sync(0xFFFFFFFFu, c.lq, l);
         PromptUnit u;
         u.kvh = head / a.head_chunks;
         const int chunk = head % a.head_chunks;
         u.head0 = u.kvh * group + chunk * a.tile_heads;
         u.nheads = min(a.tile_heads, group - chunk * a.tile_heads);
-        const int q0 = a.cu_q[seq], lq = a.cu_q[seq + 1] - q0, first = inside * 2 * a.tile_tokens;
-        u.tok0 = q0 + first;
+        u.tok0 = __shfl_sync(0xFFFFFFFFu, c.q0, l) + first;
         u.ntok = min(2 * a.tile_tokens, lq - first);
-        u.k0 = a.cu_k[seq];
-        u.lk = a.cu_k[seq + 1] - u.k0;
+        u.k0 = __shfl_sync(0xFFFFFFFFu, c.k0, l);
+        u.lk = __shfl_sync(0xFFFFFFFFu, c.lk, l);
         u.lim0 = first + 1 + u.lk - lq;
         u.n[0] = (prompt_limit(u, a.causal, min(u.ntok, a.tile_tokens) - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS;
         u.n[1] = u.ntok > a.tile_tokens ? (prompt_limit(u, a.causal, u.ntok - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
@@ -379,89 +425,112 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int w = 0; w < 2; ++w)
           if (q_use[w]) mbar_wait(&q_full[w], (q_use[w] - 1) & 1u, &never, SITE_DRAIN);
       }
-    } else if (warp == 9 && lane == 0) {
+    } else if (warp == 9) {
       // ------------------------------------------------------ matrix products
+      // The whole warp walks through this together and one elected lane issues:
+      // operands then come from uniform registers.  From inside a branch of one
+      // lane the same eight products took 600 to 900 cycles to issue, longer
+      // than they take to run.
       const uint32_t idesc_s = idesc_bf16_f32(128, 128);
       const uint32_t idesc_o = idesc_bf16_f32(128, D) | IDESC_B_MN_MAJOR;
-      const uint32_t q_addr = smem_addr(smem), ring = smem_addr(smem + SM::RING);
-      uint32_t it = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
-      auto scores = [&](int w, uint32_t stage) {
-        const uint32_t qd = kmajor_desc(q_addr + w * SM::TILE), kd = kmajor_desc(ring + stage * SM::TILE);
+      const uint32_t tm = __shfl_sync(0xFFFFFFFFu, tmem, 0);
+      const uint32_t qd = __shfl_sync(0xFFFFFFFFu, kmajor_desc(smem_addr(smem)), 0);
+      const uint32_t kd = __shfl_sync(0xFFFFFFFFu, kmajor_desc(smem_addr(smem + SM::RING)), 0);
+      const uint32_t vd = __shfl_sync(0xFFFFFFFFu, mnmajor_desc(smem_addr(smem + SM::RING), 16384), 0);
+      auto scores = [&](int w, uint32_t stage, bool last) {
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          // 32 bytes along a 128-byte line; the second half of the row is 16 KB on
-          const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * 2;
-          mma_ss(tmem + TM_S + w * 128, qd + off, kd + off, idesc_s, k > 0);
+          for (int k = 0; k < D / 16; ++k) {
+            // 32 bytes along a 128-byte line; the second half of the row is 16 KB on
+            const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * 2;
+            mma_ss(tm + TM_S + w * 128, qd + w * (SM::TILE >> 4) + off, kd + stage * (SM::TILE >> 4) + off, idesc_s, k > 0);
+          }
+          mma_commit(&s_full[w]);
+          if (last) mma_commit(&q_empty[w]);
         }
-        mma_commit(&s_full[w]);
       };
       auto values = [&](int w, uint32_t stage, bool accumulate) {
-        const uint32_t vd = mnmajor_desc(ring + stage * SM::TILE, 16384);
+        if (elect_one()) {
 #pragma unroll
-        for (int k = 0; k < PROMPT_KEYS / 16; ++k)  // 16 keys: 16 lines of 128 bytes
-          mma_ts(tmem + TM_O + w * 128, tmem + TM_S + w * 128 + k * 8, vd + k * (2048 >> 4), idesc_o, accumulate || k > 0);
-        mma_commit(&o_done[w]);
+          for (int k = 0; k < PROMPT_KEYS / 16; ++k)  // 16 keys: 16 lines of 128 bytes
+            mma_ts(tm + TM_O + w * 128, tm + TM_S + w * 128 + k * 8, vd + stage * (SM::TILE >> 4) + k * (2048 >> 4), idesc_o,
+                   accumulate || k > 0);
+          mma_commit(&o_done[w]);
+        }
+      };
+      auto release = [&](uint32_t stage) {
+        if (elect_one()) mma_commit(&kv_empty[stage]);
+      };
+      auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
+        return __all_sync(0xFFFFFFFFu, prompt_wait(bar, parity, abort_flag, busy, site));
+      };
+      uint32_t stage = 0, phase = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
+      auto advance = [&](uint32_t& st, uint32_t& ph) {
+        if (++st == S) st = 0, ph ^= 1u;
       };
       bool ok = true;
       for (uint32_t n_info = 0; ok; ++n_info) {
-        ok = prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 2);
+        ok = wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, SITE_ATTN + 2);
         if (!ok) break;
-        const int n0 = info[n_info & 1u].n[0], n1 = info[n_info & 1u].n[1];
+        const int n0 = __shfl_sync(0xFFFFFFFFu, info[n_info & 1u].n[0], 0);
+        const int n1 = __shfl_sync(0xFFFFFFFFu, info[n_info & 1u].n[1], 0);
         if (n0 < 0) break;
-        mbar_arrive(&info_empty[n_info & 1u]);
+        if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
+        __syncwarp();
         const int n = max(n0, n1), nw[2] = {n0, n1};
         if (n == 0) continue;
-        ok = prompt_wait(&kv_full[it % S], (it / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+        ok = wait(&kv_full[stage], phase, SITE_ATTN + 2);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (!ok || nw[w] == 0) continue;
-          ok = prompt_wait(&q_full[w], q_use[w] & 1u, abort_flag, busy, SITE_ATTN + 2);
+          ok = wait(&q_full[w], q_use[w] & 1u, SITE_ATTN + 2);
           ++q_use[w];
           if (!ok) continue;
           tc_fence_after();
-          scores(w, it % S);
-          if (nw[w] == 1) mma_commit(&q_empty[w]);
+          scores(w, stage, nw[w] == 1);
         }
         if (!ok) break;
-        mma_commit(&kv_empty[it % S]);
-        ++it;
+        release(stage);
+        advance(stage, phase);
         for (int j = 0; j < n && ok; ++j) {
-          const uint32_t sv = it % S, sk = (it + 1) % S;
-          ok = prompt_wait(&kv_full[sv], (it / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+          uint32_t sk = stage, phase_k = phase;  // values at `stage`, the next keys behind them
+          advance(sk, phase_k);
+          ok = wait(&kv_full[stage], phase, SITE_ATTN + 2);
           bool have_k = false;
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (!ok || j >= nw[w]) continue;
-            ok = prompt_wait(&p_full[w], p_use[w] & 1u, abort_flag, busy, SITE_ATTN + 3);
+            ok = wait(&p_full[w], p_use[w] & 1u, SITE_ATTN + 3);
             ++p_use[w];
             if (!ok) continue;
             tc_fence_after();
-            values(w, sv, j > 0);
+            values(w, stage, j > 0);
             if (j + 1 < nw[w]) {
-              if (!have_k) ok = prompt_wait(&kv_full[sk], ((it + 1) / S) & 1u, abort_flag, busy, SITE_ATTN + 2);
+              if (!have_k) ok = wait(&kv_full[sk], phase_k, SITE_ATTN + 2);
               have_k = true;
               if (!ok) continue;
-              scores(w, sk);
-              if (j + 2 == nw[w]) mma_commit(&q_empty[w]);
+              scores(w, sk, j + 2 == nw[w]);
             }
           }
           if (!ok) break;
-          mma_commit(&kv_empty[sv]);
-          ++it;
+          release(stage);
           if (j + 1 < n) {
-            mma_commit(&kv_empty[sk]);
-            ++it;
+            release(sk);
+            stage = sk, phase = phase_k;
           }
+          advance(stage, phase);
         }
       }
       // every product issued must be complete before tensor memory is released
-      mma_commit(drain);
-      int never = 0;
-      mbar_wait(drain, 0u, &never, SITE_DRAIN);
+      if (elect_one()) {
+        mma_commit(drain);
+        int never = 0;
+        mbar_wait(drain, 0u, &never, SITE_DRAIN);
+      }
     }
   } else {
     // -------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(216));  // 2 x 216 + 72 <= 3 x 168
     const int w = warp >> 2;
     const int row = (warp & 3) * 32 + lane;
     const int tok = row / a.tile_heads, hd = row - tok * a.tile_heads;
@@ -490,12 +559,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         for (int x = 0; x < 4; ++x) tmem_ld_32x32b_x32(t_s + 32 * x, s[x]);
         tmem_ld_wait();
         if ((j + 1) * PROMPT_KEYS > warp_lim) {
-          const int rel = lim - j * PROMPT_KEYS;
+          const int rel = lim - j * PROMPT_KEYS, warp_rel = warp_lim - j * PROMPT_KEYS;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
+            if (32 * (x + 1) > warp_rel) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (32 * x + e >= rel) s[x][e] = 0xFF800000u;  // -inf
+              for (int e = 0; e < 32; ++e)
+                if (32 * x + e >= rel) s[x][e] = 0xFF800000u;  // -inf
+            }
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -534,20 +605,24 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint32_t* in = &s[x][2 * e];
             float lo, hi;
             unpack2(fma2(pack2(__uint_as_float(in[0]), __uint_as_float(in[1])), c2, shift2), lo, hi);
-            lo = ex2(lo);
-            hi = ex2(hi);
+            if (e % PROMPT_POLY == PROMPT_POLY - 1) {
+              unpack2(exp2_poly2(lo, hi), lo, hi);
+            } else {
+              lo = ex2(lo);
+              hi = ex2(hi);
+            }
             sum2[e & 1] = add2(sum2[e & 1], pack2(lo, hi));
             p[e] = cvt_bf16x2(lo, hi);
           }
           tmem_st_x16(t_s + 16 * x, p);
         }
-        float s0, s1;
-        unpack2(add2(sum2[0], sum2[1]), s0, s1);
-        l += s0 + s1;
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&p_full[w]);
+        float s0, s1;
+        unpack2(add2(sum2[0], sum2[1]), s0, s1);
+        l += s0 + s1;
       }
       if (!ok) break;
       // ---- result
@@ -563,17 +638,23 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           tmem_ld_32x32b_x32(t_o + 32 * x, o);
           tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
+          for (int e = 0; e < 32; ++e) {
+            const float f = lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+            bad |= f != f;
+            o[e] = __float_as_uint(f);
+          }
+          uint32_t r[16];
 #pragma unroll
-            for (int y = 0; y < 8; ++y) {
-              f[y] = lim > 0 ? __uint_as_float(o[e + y]) * inv : 0.f;
-              bad |= f[y] != f[y];
+          for (int e = 0; e < 16; ++e) r[e] = cvt_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
+          if (valid) {
+            if (a.wide) {
+              st_global_32(out + 32 * x, r);
+              st_global_32(out + 32 * x + 16, r + 8);
+            } else {
+#pragma unroll
+              for (int e = 0; e < 16; e += 4)
+                *reinterpret_cast<uint4*>(out + 32 * x + 2 * e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
             }
-            if (valid)
-              *reinterpret_cast<uint4*>(out + 32 * x + e) =
-                  make_uint4(cvt_bf16x2(f[0], f[1]), cvt_bf16x2(f[2], f[3]), cvt_bf16x2(f[4], f[5]),
-                             cvt_bf16x2(f[6], f[7]));
           }
         }
         tc_fence_before();

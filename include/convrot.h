@@ -353,7 +353,7 @@ convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M
  *
  * Tensors of head rows are bf16 [rows, heads, D] with D = 64 or 128, heads
  * and elements contiguous and `*_stride` elements from one row to the next (a
- * multiple of 8, at least heads * D), so column views of a fused q/k/v output
+ * multiple of 8, at least heads * D, at most 2^26), so column views of a fused q/k/v output
  * are taken as they are.  Query head h reads key/value head h / (q_heads /
  * kv_heads); q_heads % kv_heads == 0, q_heads <= 1024.
  *

@@ -15,8 +15,9 @@ constexpr int kMaxPage = 4096;
 bool heads_ok(int q_heads, int kv_heads) {
   return q_heads > 0 && kv_heads > 0 && q_heads <= kMaxHeads && q_heads % kv_heads == 0;
 }
+constexpr int64_t kMaxStride = 1 << 26;  // offsets inside a tile's rows stay below 2^32
 bool stride_ok(int64_t stride, int heads, int D, int rows) {
-  return stride % 8 == 0 && (rows <= 1 || stride >= static_cast<int64_t>(heads) * D);
+  return stride % 8 == 0 && stride <= kMaxStride && (rows <= 1 || stride >= static_cast<int64_t>(heads) * D);
 }
 
 convrot_status run_append(const AppendArgs& args, int D, bool int8, cudaStream_t st) {
@@ -59,7 +60,6 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   a.head_chunks = (group + 127) / 128;
   a.tile_heads = (group + a.head_chunks - 1) / a.head_chunks;
   a.tile_tokens = 128 / a.tile_heads;
-  a.wide = aligned(a.o, 32) && a.o_stride % 16 == 0;
   CUtensorMap mq, mk, mv;
   if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, D, a.q_stride, a.tile_heads, a.tile_tokens))
     return CONVROT_ERR_CUDA;

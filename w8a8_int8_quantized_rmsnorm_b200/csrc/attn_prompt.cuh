@@ -45,21 +45,25 @@ struct PromptArgs {
   int head_chunks;                                 // tiles side by side for one group
   float scale_log2;                                // scale * log2(e)
   int causal;
-  int wide;                                        // result rows lie on 32-byte boundaries
 };
 
 constexpr int PROMPT_KEYS = 128;     // keys per tile
-constexpr int PROMPT_POLY = 1000;       // one pair of exp2 in so many is a polynomial
+constexpr int PROMPT_HALF = 64;      // a last tile of no more keys than this is half a tile
 constexpr int PROMPT_THREADS = 384;  // 2 softmax warpgroups, 1 of fetch + issue
 constexpr unsigned SITE_ATTN = 9;    // wait sites SITE_ATTN .. SITE_ATTN + 5
 
 template <int D>
 struct PromptSmem {
   static constexpr int TILE = 128 * D * 2;                // bytes of a Q, K or V tile
-  static constexpr int STAGES = D == 128 ? 5 : 10;
+  static constexpr int STAGES = D == 128 ? 4 : 8;
+  // One pair of exp2 in so many is a polynomial.  With D = 64 the exponential
+  // unit (16 a cycle) bounds: 4 x 1024 heads x tokens took 102 us without and 96
+  // us with; with D = 128 the tensor core does, and nothing was gained.
+  static constexpr int POLY = D == 128 ? 1 << 20 : 4;
   static constexpr int RING = 2 * TILE;
-  static constexpr int BARS = RING + STAGES * TILE;
-  static constexpr int N_BARS = 2 * STAGES + 15;
+  static constexpr int OUT = RING + STAGES * TILE;        // 4 KB per softmax warp: 32 rows of 64 elements
+  static constexpr int BARS = OUT + 8 * 4096;
+  static constexpr int N_BARS = 2 * STAGES + 17;
   static constexpr int INFO = BARS + 8 * N_BARS;
   static constexpr int MISC = INFO + 2 * 48;
   static constexpr int TOTAL = MISC + 16 + 1024;          // + alignment of the first tile
@@ -73,7 +77,7 @@ struct PromptUnit {
   int head0;       // first query head
   int nheads;      // query heads of the unit
   int kvh;
-  int n[2];        // key tiles of the two row tiles; n[0] = -1: no more units
+  int n[2];        // half key tiles of the two row tiles; n[0] = -1: no more units
   int pad[2];
 };
 static_assert(sizeof(PromptUnit) == 48, "unit layout");
@@ -140,17 +144,15 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-// 32 bytes, a whole sector: a thread stores a row of its own, and half a
-// sector at a time takes twice as many passes through the store path.
-__device__ __forceinline__ void st_global_32(void* p, const uint32_t* r) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]),
-               "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
-               : "memory");
-}
-
 __device__ __forceinline__ float ex2(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
   return r;
 }
 
@@ -279,7 +281,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::BARS);
   uint64_t *kv_full = bars, *kv_empty = bars + S, *q_full = bars + 2 * S, *q_empty = q_full + 2,
            *s_full = q_full + 4, *p_full = q_full + 6, *o_done = q_full + 8, *info_full = q_full + 10,
-           *info_empty = q_full + 12, *drain = q_full + 14;
+           *info_empty = q_full + 12, *drain = q_full + 14, *p_rest = q_full + 15;
   PromptUnit* info = reinterpret_cast<PromptUnit*>(smem + SM::INFO);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -296,7 +298,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       mbar_init(&q_full[i], 1);
       mbar_init(&q_empty[i], 1);
       mbar_init(&s_full[i], 1);
-      mbar_init(&p_full[i], 4);
+      mbar_init(&p_full[i], 4);  // a tile's probabilities come in two halves
+      mbar_init(&p_rest[i], 4);
       mbar_init(&o_done[i], 1);
       mbar_init(&info_full[i], 1);
       mbar_init(&info_empty[i], 9);  // the issuing warp and the eight softmax warps
@@ -371,8 +374,8 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         u.k0 = __shfl_sync(0xFFFFFFFFu, c.k0, l);
         u.lk = __shfl_sync(0xFFFFFFFFu, c.lk, l);
         u.lim0 = first + 1 + u.lk - lq;
-        u.n[0] = (prompt_limit(u, a.causal, min(u.ntok, a.tile_tokens) - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS;
-        u.n[1] = u.ntok > a.tile_tokens ? (prompt_limit(u, a.causal, u.ntok - 1) + PROMPT_KEYS - 1) / PROMPT_KEYS : 0;
+        u.n[0] = (prompt_limit(u, a.causal, min(u.ntok, a.tile_tokens) - 1) + PROMPT_HALF - 1) / PROMPT_HALF;
+        u.n[1] = u.ntok > a.tile_tokens ? (prompt_limit(u, a.causal, u.ntok - 1) + PROMPT_HALF - 1) / PROMPT_HALF : 0;
         u.pad[0] = u.pad[1] = 0;
         if (lane == 0) {
           const uint32_t slot = n_info & 1u;
@@ -402,7 +405,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
                           u.k0 + j * PROMPT_KEYS);
             ++it;
           };
-          const int n = max(u.n[0], u.n[1]);
+          const int n = (max(u.n[0], u.n[1]) + 1) / 2;
           load_q(0);
           if (n > 0) load_kv(&tm_k, 0);
           load_q(1);
@@ -449,70 +452,73 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           if (last) mma_commit(&q_empty[w]);
         }
       };
-      auto values = [&](int w, uint32_t stage, bool accumulate) {
+      auto values = [&](int w, uint32_t stage, int half, bool accumulate) {  // 64 keys
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < PROMPT_KEYS / 16; ++k)  // 16 keys: 16 lines of 128 bytes
+          for (int x = 0; x < 4; ++x) {  // 16 keys: 16 lines of 128 bytes
+            const int k = 4 * half + x;
             mma_ts(tm + TM_O + w * 128, tm + TM_S + w * 128 + k * 8, vd + stage * (SM::TILE >> 4) + k * (2048 >> 4), idesc_o,
-                   accumulate || k > 0);
-          mma_commit(&o_done[w]);
+                   accumulate || x > 0);
+          }
+          if (half) mma_commit(&o_done[w]);
         }
       };
       auto release = [&](uint32_t stage) {
         if (elect_one()) mma_commit(&kv_empty[stage]);
       };
-      auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) -> bool {
-        return __all_sync(0xFFFFFFFFu, prompt_wait(bar, parity, abort_flag, busy, site));
-      };
-      uint32_t stage = 0, phase = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0};
+      // A wait that gives up has raised the abort flag, which the warp looks at
+      // together, once per tile: until then it issues on without harm, since a
+      // product touches this CTA's own memory only.
+      auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) { prompt_wait(bar, parity, abort_flag, busy, site); };
+      auto going = [&]() -> bool { return __all_sync(0xFFFFFFFFu, *abort_flag == 0); };
+      uint32_t stage = 0, phase = 0, q_use[2] = {0, 0}, p_use[2] = {0, 0}, rest_use[2] = {0, 0};
       auto advance = [&](uint32_t& st, uint32_t& ph) {
         if (++st == S) st = 0, ph ^= 1u;
       };
-      bool ok = true;
-      for (uint32_t n_info = 0; ok; ++n_info) {
-        ok = wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, SITE_ATTN + 2);
-        if (!ok) break;
+      for (uint32_t n_info = 0;; ++n_info) {
+        wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, SITE_ATTN + 2);
+        if (!going()) break;
         const int n0 = __shfl_sync(0xFFFFFFFFu, info[n_info & 1u].n[0], 0);
         const int n1 = __shfl_sync(0xFFFFFFFFu, info[n_info & 1u].n[1], 0);
         if (n0 < 0) break;
         if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
         __syncwarp();
-        const int n = max(n0, n1), nw[2] = {n0, n1};
+        const int nh[2] = {n0, n1}, nw[2] = {(n0 + 1) / 2, (n1 + 1) / 2}, n = max(nw[0], nw[1]);
         if (n == 0) continue;
-        ok = wait(&kv_full[stage], phase, SITE_ATTN + 2);
+        wait(&kv_full[stage], phase, SITE_ATTN + 2);
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          if (!ok || nw[w] == 0) continue;
-          ok = wait(&q_full[w], q_use[w] & 1u, SITE_ATTN + 2);
+          if (nw[w] == 0) continue;
+          wait(&q_full[w], q_use[w] & 1u, SITE_ATTN + 2);
           ++q_use[w];
-          if (!ok) continue;
           tc_fence_after();
           scores(w, stage, nw[w] == 1);
         }
-        if (!ok) break;
         release(stage);
         advance(stage, phase);
-        for (int j = 0; j < n && ok; ++j) {
+        int j = 0;
+        for (; j < n && going(); ++j) {
           uint32_t sk = stage, phase_k = phase;  // values at `stage`, the next keys behind them
           advance(sk, phase_k);
-          ok = wait(&kv_full[stage], phase, SITE_ATTN + 2);
-          bool have_k = false;
+          wait(&kv_full[stage], phase, SITE_ATTN + 2);
+          if (j + 1 < n) wait(&kv_full[sk], phase_k, SITE_ATTN + 2);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (!ok || j >= nw[w]) continue;
-            ok = wait(&p_full[w], p_use[w] & 1u, SITE_ATTN + 3);
+            if (j >= nw[w]) continue;
+            wait(&p_full[w], p_use[w] & 1u, SITE_ATTN + 3);
             ++p_use[w];
-            if (!ok) continue;
             tc_fence_after();
-            values(w, stage, j > 0);
-            if (j + 1 < nw[w]) {
-              if (!have_k) ok = wait(&kv_full[sk], phase_k, SITE_ATTN + 2);
-              have_k = true;
-              if (!ok) continue;
-              scores(w, sk, j + 2 == nw[w]);
+            values(w, stage, 0, j > 0);
+            if (2 * j + 2 > nh[w]) {  // a last tile's first half is all there is
+              if (elect_one()) mma_commit(&o_done[w]);
+              continue;
             }
+            wait(&p_rest[w], rest_use[w] & 1u, SITE_ATTN + 3);
+            ++rest_use[w];
+            tc_fence_after();
+            values(w, stage, 1, true);
+            if (j + 1 < nw[w]) scores(w, sk, j + 2 == nw[w]);
           }
-          if (!ok) break;
           release(stage);
           if (j + 1 < n) {
             release(sk);
@@ -520,6 +526,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
           advance(stage, phase);
         }
+        if (j < n) break;
       }
       // every product issued must be complete before tensor memory is released
       if (elect_one()) {
@@ -542,7 +549,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (!prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 4)) break;
       const PromptUnit& u = info[n_info & 1u];  // read where it is needed: registers are short
       if (u.n[0] < 0) break;
-      const int n_tiles = u.n[w];
+      const int n_halves = u.n[w], n_tiles = (n_halves + 1) / 2;
       const int i = w * a.tile_tokens + tok;  // token of the unit
       const bool valid = tok < a.tile_tokens && i < u.ntok && hd < u.nheads;
       // rows that are not stored mask nothing
@@ -570,9 +577,9 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; ++e)
+        for (int e = 0; e < 32; e += 2)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top[x] = fmaxf(top[x], __uint_as_float(s[x][e]));
+          for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         if (j == 0) {
           m = high;
@@ -599,13 +606,14 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         uint64_t sum2[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
+          if (x >= 2 && 2 * j + 2 > n_halves) break;  // the same for the whole warpgroup
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
             const uint32_t* in = &s[x][2 * e];
             float lo, hi;
             unpack2(fma2(pack2(__uint_as_float(in[0]), __uint_as_float(in[1])), c2, shift2), lo, hi);
-            if (e % PROMPT_POLY == PROMPT_POLY - 1) {
+            if (e % SM::POLY == SM::POLY - 1) {
               unpack2(exp2_poly2(lo, hi), lo, hi);
             } else {
               lo = ex2(lo);
@@ -615,53 +623,66 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             p[e] = cvt_bf16x2(lo, hi);
           }
           tmem_st_x16(t_s + 16 * x, p);
+          if (x & 1) {  // half of the keys: the product with their values may begin
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(x == 1 ? &p_full[w] : &p_rest[w]);
+          }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[w]);
         float s0, s1;
         unpack2(add2(sum2[0], sum2[1]), s0, s1);
         l += s0 + s1;
       }
       if (!ok) break;
       // ---- result
-      uint16_t* out = a.o + static_cast<int64_t>(u.tok0 + i) * a.o_stride + static_cast<int64_t>(u.head0 + hd) * D;
+      // A thread holds a row; stored as they are, 32 rows at a time, the pieces
+      // of a warp's store would lie in 32 lines.  So the warp turns 64 elements of
+      // its rows at a time in shared memory and stores whole 128-byte lines.
+      const uint32_t out_off = static_cast<uint32_t>(i) * static_cast<uint32_t>(a.o_stride / 8) + hd * (D / 8);  // 16-byte pieces
+      uint16_t* out = a.o + static_cast<int64_t>(u.tok0) * a.o_stride + static_cast<int64_t>(u.head0) * D;
+      const unsigned stored = __ballot_sync(0xFFFFFFFFu, valid);
       bool bad = false;
       if (n_tiles > 0) {
         if (!prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
         tc_fence_after();
-        const float inv = lim > 0 ? 1.f / l : 0.f;
+      }
+      const float inv = lim > 0 ? 1.f / l : 0.f;
+      const uint32_t mine = smem_addr(smem + SM::OUT + warp * 4096);
 #pragma unroll
-        for (int x = 0; x < D / 32; ++x) {
-          uint32_t o[32];
-          tmem_ld_32x32b_x32(t_o + 32 * x, o);
-          tmem_ld_wait();
+      for (int x = 0; x < D / 64; ++x) {
 #pragma unroll
-          for (int e = 0; e < 32; ++e) {
-            const float f = lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
+        for (int y = 0; y < 4; ++y) {
+          uint32_t o[16];
+          if (n_tiles > 0) {
+            tmem_ld_x16(t_o + 64 * x + 16 * y, o);
+            tmem_ld_wait();
+          }
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float f = n_tiles > 0 && lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
             bad |= f != f;
             o[e] = __float_as_uint(f);
           }
-          uint32_t r[16];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) r[e] = cvt_bf16x2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1]));
-          if (valid) {
-            if (a.wide) {
-              st_global_32(out + 32 * x, r);
-              st_global_32(out + 32 * x + 16, r + 8);
-            } else {
+          for (int e = 0; e < 2; ++e) {
+            uint32_t r[4];
 #pragma unroll
-              for (int e = 0; e < 16; e += 4)
-                *reinterpret_cast<uint4*>(out + 32 * x + 2 * e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
-            }
+            for (int z = 0; z < 4; ++z) r[z] = cvt_bf16x2(__uint_as_float(o[8 * e + 2 * z]), __uint_as_float(o[8 * e + 2 * z + 1]));
+            sts128(mine + lane * 128 + (((2 * y + e) ^ (lane & 7)) << 4), r[0], r[1], r[2], r[3]);
           }
         }
-        tc_fence_before();
-      } else if (valid) {
+        __syncwarp();
 #pragma unroll
-        for (int e = 0; e < D; e += 8) *reinterpret_cast<uint4*>(out + e) = make_uint4(0, 0, 0, 0);
+        for (int y = 0; y < 8; ++y) {  // four rows at a time, eight lanes a row
+          const int r = 4 * y + (lane >> 3);
+          const uint4 v = lds128(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          const uint32_t off = __shfl_sync(0xFFFFFFFFu, out_off, r);
+          if ((stored >> r) & 1u) *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(off) + 8 * x + (lane & 7)) * 8) = v;
+        }
+        __syncwarp();
       }
+      if (n_tiles > 0) tc_fence_before();
       unsigned again = __ballot_sync(0xFFFFFFFFu, bad && valid);
       if (again) {
         if (lane == 0) atomicAdd(const_cast<int*>(busy), 1);

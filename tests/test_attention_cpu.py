@@ -191,6 +191,31 @@ def test_append_operands():
     call("k_out must have 3 rows", k_out=bf(T + 1, Hkv, D))
 
 
+def test_append_cache_heads():
+    T, D = 3, 64
+    slots, cache = torch.zeros(T, dtype=torch.int64), bf(5, 2, 16, D)
+    for heads in (1, 4):
+        _raises("k_cache must hold", cr.convrot_rope_append, bf(T, 4, D), bf(T, heads, D), bf(T, heads, D), f32(9, 64), i32(T),
+                slots, cache, cache)
+    _raises("k_cache must hold", cr.convrot_rope_append, bf(T, 4, 128), bf(T, 2, 128), bf(T, 2, 128), f32(9, 64), i32(T), slots,
+            cache, cache)
+
+
+def test_rope_table_matches_the_oracle():
+    t = cr.rope_table(1000, 64, 1e4)
+    assert t.dtype == torch.float32 and np.abs(t.numpy() - ref.rope_table(1000, 64, 1e4)).max() <= 2.0 ** -23
+
+
+def test_attention_block_shapes():
+    W = [torch.zeros(n, 512, dtype=torch.bfloat16) for n in (512, 128, 128)]
+    with pytest.raises(ValueError, match="multiple of kv_heads"):
+        cr.ConvRotAttention(*W, W[0], q_heads=8, kv_heads=3, rope=f32(4, 64))
+    with pytest.raises(ValueError, match="Wk and Wv must have"):
+        cr.ConvRotAttention(*W, W[0], q_heads=8, kv_heads=4, rope=f32(4, 64))
+    with pytest.raises(ValueError, match="Wo must have"):
+        cr.ConvRotAttention(*W, torch.zeros(512, 256, dtype=torch.bfloat16), q_heads=8, kv_heads=2, rope=f32(4, 64))
+
+
 def test_prompt_operands():
     q, k, cu = bf(6, 4, 64), bf(6, 2, 64), i32(3)
     f = cr.convrot_attention_prompt

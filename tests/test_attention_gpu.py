@@ -557,3 +557,91 @@ def test_decode_leaves_its_workspace_zero(cr):
         c = decode_case(50, lens, 8, 2, 128, 16, False)
         check_decode(cr, c, lens, workspace=ws)
         assert not ws.buf.any()
+
+
+# ------------------------------------------------------------------ together
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv,page", [(128, 8, 2, 16), (64, 8, 4, 64)])
+def test_attention_block_prompts_then_tokens(cr, D, Hq, Hkv, page, i8):
+    """ConvRotAttention over packed prompts, then two decode steps of all
+    sequences: the wiring against the operators one by one, the operators
+    against the oracle, each on the inputs it got."""
+    hidden, lens = 512, [70, 3, 129]
+    W = [randn(60 + i, n, hidden, std=0.05) for i, n in enumerate((Hq * D, Hkv * D, Hkv * D))]
+    Wo = randn(63, hidden, Hq * D, std=0.05)
+    g = torch.Generator().manual_seed(1)
+    norms = [torch.randn(D, generator=g).cuda() * 0.1 for _ in range(2)]
+    rope = cr.rope_table(200, D, device="cuda")
+    layer = cr.ConvRotAttention(*W, Wo, q_heads=Hq, kv_heads=Hkv, rope=rope, norm_w=torch.zeros(hidden).cuda(),
+                                q_norm=norms[0], k_norm=norms[1])
+    need = [-(-(n + 2) // page) for n in lens]
+    cache = cr.PagedKVCache(sum(need) + 1, Hkv, D, page_size=page, int8=i8)
+    table = torch.full((len(lens), max(need)), -1, dtype=torch.int32)
+    perm, at = torch.randperm(sum(need) + 1, generator=g), 0
+    for i, n in enumerate(need):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    table = table.cuda()
+    seq = torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens)).cuda()
+    pos = torch.cat([torch.arange(n) for n in lens]).int().cuda()
+    cu = torch.tensor([0] + lens).cumsum(0).int().cuda()
+
+    def pieces(x, pos, slots, rotated):
+        q, k, v = (t.unflatten(1, (-1, D)).clone() for t in layer.qkv(x))
+        c = dict(q=q, k=k, v=v, rope=rope, positions=pos, slots=slots, q_norm=norms[0], k_norm=norms[1],
+                 k_cache=cache.k.clone(), v_cache=cache.v.clone())
+        if i8:
+            c |= dict(k_scale=cache.k_scale.clone(), v_scale=cache.v_scale.clone())
+        before = {n: t.clone() for n, t in c.items()}
+        qo, ko = cr.convrot_rope_append(**c, k_out=torch.empty_like(k) if rotated else None)
+        check_append(c, before, qo, ko)
+        return c, qo, ko
+
+    def same_cache(c):
+        assert torch.equal(cache.k, c["k_cache"]) and torch.equal(cache.v, c["v_cache"])
+        if i8:
+            assert torch.equal(cache.k_scale, c["k_scale"]) and torch.equal(cache.v_scale, c["v_scale"])
+
+    x = randn(64, sum(lens), hidden)
+    slots = cache.slots(table, seq, pos)
+    c, q, k = pieces(x, pos, slots, True)
+    o = cr.convrot_attention_prompt(q, k, c["v"], cu)
+    want, tol = ref.packed_attention(f64(q), f64(k), f64(c["v"]), cu.tolist(), cu.tolist(), D ** -0.5, True)
+    within(f64(o), want, tol, "prompt")
+    y = layer.prompt(x, cu, pos, slots, cache)
+    assert y.shape == (sum(lens), hidden) and torch.equal(y, layer.o(o.flatten(1)))
+    same_cache(c)
+    for step in range(2):
+        x = randn(65 + step, len(lens), hidden)
+        now = torch.tensor([n + step for n in lens], dtype=torch.int32).cuda()
+        slots = cache.slots(table, torch.arange(len(lens)).cuda(), now)
+        c, q, _ = pieces(x, now, slots, False)
+        a = dict(q=q, k_cache=c["k_cache"], v_cache=c["v_cache"], block_table=table, seq_lens=now + 1)
+        if i8:
+            a |= dict(k_scale=c["k_scale"], v_scale=c["v_scale"])
+        o = check_decode(cr, a, (now + 1).tolist())
+        y = layer.decode(x, now, slots, cache, table, now + 1)
+        assert torch.equal(y, layer.o(o.flatten(1)))
+        same_cache(c)
+    assert cr.convrot_device_status() == 0
+
+
+def test_decode_step_agrees_with_the_prompt_s_last_row(cr):
+    """The last row of a prompt's attention and the same token decoded over the
+    cache are the same sum: both within their bounds of the oracle's value."""
+    n, Hq, Hkv, D, page = 300, 8, 2, 128, 16
+    c = append_case(70, n, Hq, Hkv, D, D, page, False, False, rows=n)
+    c["positions"] = torch.arange(n, dtype=torch.int32).cuda()
+    pages = c["k_cache"].shape[0]
+    table = torch.randperm(pages, generator=torch.Generator().manual_seed(2))[None].int()
+    run = torch.arange(n)
+    c["slots"] = (table[0, run // page].long() * page + run % page).cuda()
+    ko = torch.empty(n, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    q, k = cr.convrot_rope_append(**c, k_out=ko)
+    cu = torch.tensor([0, n], dtype=torch.int32).cuda()
+    a = cr.convrot_attention_prompt(q, k, c["v"], cu)[-1]
+    b = cr.convrot_attention_decode(q[-1:], c["k_cache"], c["v_cache"], table.cuda(),
+                                    torch.tensor([n], dtype=torch.int32).cuda())[0]
+    o, tol = ref.packed_attention(f64(q[-1:]), f64(k), f64(c["v"]), [0, 1], [0, n], D ** -0.5, True)
+    within(f64(a), o[0], tol[0], "prompt")
+    within(f64(b), o[0], tol[0], "decode")

@@ -27,6 +27,7 @@ __all__ = [
     "convrot_rope_append", "convrot_attention_prompt",
     "convrot_attention_decode_workspace_bytes", "convrot_attention_decode",
     "Workspace", "ConvRotLinear", "ConvRotFusedLinear", "ConvRotMLP",
+    "rope_table", "PagedKVCache", "ConvRotAttention",
 ]
 
 
@@ -696,3 +697,80 @@ class ConvRotMLP:
         return convrot_int8_linear(Hq, s_h, self.Wq_d, self.s_d, out, self.workspace)
 
     __call__ = forward
+
+
+def rope_table(rows: int, dim: int, theta: float = 1e6, device=None) -> torch.Tensor:
+    """fp32 [rows, dim]: cosines, then sines, of position * theta^(-2 i / dim),
+    the angles taken in fp64 (an fp32 angle is off by 2^-24 of itself, which at
+    position 10^6 is 0.06 of a radian)."""
+    freq = theta ** (-torch.arange(0, dim, 2, dtype=torch.float64, device=device) / dim)
+    angle = torch.arange(rows, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+class PagedKVCache:
+    """One layer's keys and values in pages of page_size tokens: bf16, or int8
+    with one fp32 scale per token and head.  Which sequence owns which page is
+    the caller's block table (int32 [sequences, pages per sequence])."""
+
+    def __init__(self, pages: int, kv_heads: int, head_dim: int, *, page_size: int = 64, int8: bool = False,
+                 device=None):
+        dev = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        shape = (pages, kv_heads, page_size, head_dim)
+        self.page_size = page_size
+        self.k, self.v = (torch.zeros(shape, dtype=torch.int8 if int8 else torch.bfloat16, device=dev) for _ in range(2))
+        self.k_scale, self.v_scale = ((torch.zeros(shape[:3], device=dev) for _ in range(2)) if int8 else (None, None))
+
+    def slots(self, block_table: torch.Tensor, sequence: torch.Tensor, position: torch.Tensor) -> torch.Tensor:
+        """Slots (int64) of tokens at `position` of rows `sequence` of the block table."""
+        page = block_table[sequence.long(), position.long() // self.page_size].long()
+        return page * self.page_size + position % self.page_size
+
+
+class ConvRotAttention:
+    """The attention block of the quantised decoder layer: one fused q/k/v
+    projection (behind the fused RMSNorm), position rotation and append to a
+    paged cache, attention, o projection.  Beside ConvRotMLP it completes the
+    layer; the four projections are the ones the model cards quantise.
+
+    rope is a rope_table (or any table of that form); q_norm and k_norm are the
+    per-head RMSNorm weights (applied as 1 + w) of models that have them.
+    """
+
+    def __init__(self, Wq: torch.Tensor, Wk: torch.Tensor, Wv: torch.Tensor, Wo: torch.Tensor, *, q_heads: int,
+                 kv_heads: int, rope: torch.Tensor, weight_bits: int = 8, group: int = 256,
+                 norm_w: Optional[torch.Tensor] = None, q_norm: Optional[torch.Tensor] = None,
+                 k_norm: Optional[torch.Tensor] = None, x_calib: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                 scale: Optional[float] = None):
+        if Wq.shape[0] % q_heads or q_heads % kv_heads:
+            raise ValueError("q_heads must divide the rows of Wq and be a multiple of kv_heads")
+        self.q_heads, self.kv_heads, self.head_dim = q_heads, kv_heads, Wq.shape[0] // q_heads
+        if Wk.shape[0] != kv_heads * self.head_dim or Wv.shape[0] != kv_heads * self.head_dim:
+            raise ValueError(f"Wk and Wv must have {kv_heads} x {self.head_dim} rows")
+        if Wo.shape[1] != Wq.shape[0]:
+            raise ValueError("Wo must have as many columns as Wq has rows")
+        self.rope, self.q_norm, self.k_norm, self.eps, self.scale = rope, q_norm, k_norm, eps, scale
+        self.qkv = ConvRotFusedLinear([Wq, Wk, Wv], weight_bits=weight_bits, group=group, norm_w=norm_w,
+                                      x_calib=x_calib, eps=eps)
+        self.o = ConvRotLinear(Wo, weight_bits=weight_bits, group=group, eps=eps)
+
+    def _append(self, x, positions, slots, cache: PagedKVCache, rotated_k: bool):
+        q, k, v = (t.unflatten(1, (-1, self.head_dim)) for t in self.qkv(x))
+        convrot_rope_append(q, k, v, self.rope, positions, slots, cache.k, cache.v, k_scale=cache.k_scale,
+                            v_scale=cache.v_scale, q_norm=self.q_norm, k_norm=self.k_norm, eps=self.eps, q_out=q,
+                            k_out=k if rotated_k else None)
+        return q, k, v
+
+    def prompt(self, x: torch.Tensor, cu_seqlens: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
+               cache: PagedKVCache) -> torch.Tensor:
+        """Whole prompts, packed one after another: x bf16 [tokens, hidden]."""
+        q, k, v = self._append(x, positions, slots, cache, True)
+        return self.o(convrot_attention_prompt(q, k, v, cu_seqlens, scale=self.scale).flatten(1))
+
+    def decode(self, x: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor, cache: PagedKVCache,
+               block_table: torch.Tensor, seq_lens: torch.Tensor) -> torch.Tensor:
+        """One new token per sequence: x bf16 [sequences, hidden]; seq_lens counts it."""
+        q, _, _ = self._append(x, positions, slots, cache, False)
+        o = convrot_attention_decode(q, cache.k, cache.v, block_table, seq_lens, k_scale=cache.k_scale,
+                                     v_scale=cache.v_scale, scale=self.scale)
+        return self.o(o.flatten(1))

@@ -422,28 +422,34 @@ def convrot_fold_row_scales(s_row: torch.Tensor, smooth: torch.Tensor) -> torch.
 
 
 # ---------------------------------------------------------------- attention
+# These calls are short on the GPU (a decode step's append takes 2 us), so their
+# checks first ask whether all is well in as few steps as there are, and look
+# for what is wrong only if it is not.
 def _heads(t: torch.Tensor, name: str, rows: Optional[int] = None, heads: Optional[int] = None,
            dim: Optional[int] = None):
     """A bf16 [rows, heads, D] operand whose heads lie next to one another; rows
-    may be further apart (a column view of a fused projection's output)."""
+    may be further apart (a column view of a fused projection's output).
+    Returns (rows, heads, D, row stride)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.dim() != 3:
         raise ValueError(f"{name} must have 3 dimensions [rows, heads, D]")
     r, h, d = t.shape
-    for got, want, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "elements per head")):
-        if want is not None and got != want:
-            raise ValueError(f"{name} must have {want} {what}, got {got}")
+    if (rows is not None and r != rows) or (heads is not None and h != heads) or (dim is not None and d != dim):
+        for got, want, what in ((r, rows, "rows"), (h, heads, "heads"), (d, dim, "elements per head")):
+            if want is not None and got != want:
+                raise ValueError(f"{name} must have {want} {what}, got {got}")
     sr, sh, sd = t.stride()
-    if t.numel() and (sd != 1 or (h > 1 and sh != d) or (r > 1 and (sr < h * d or sr % 8))):
+    if (sd != 1 or (sh != d and h > 1) or (r > 1 and (sr < h * d or sr % 8))) and t.numel():
         raise ValueError(f"{name} must have contiguous heads and rows a multiple of 8 elements apart, got strides {t.stride()}")
-    return r, h, d
+    return r, h, d, sr if r > 1 else h * d
 
 
-def _row_stride(t: torch.Tensor) -> int:
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
+def _vector(t: torch.Tensor, dtype, name: str, n: int):
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == (n,) and t.is_contiguous()):
+        _need(t, dtype, name, shape=(n,))
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale):
@@ -451,11 +457,27 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
     i8 = k_scale is not None or v_scale is not None
     dtype = torch.int8 if i8 else torch.bfloat16
     _need(k_cache, dtype, "k_cache", 4)
-    _need(v_cache, dtype, "v_cache", shape=k_cache.shape)
+    shape = k_cache.shape
+    if not (isinstance(v_cache, torch.Tensor) and v_cache.dtype is dtype and v_cache.shape == shape
+            and v_cache.is_contiguous()):
+        _need(v_cache, dtype, "v_cache", shape=shape)
     if i8:
-        _need(k_scale, torch.float32, "k_scale", shape=k_cache.shape[:3])
-        _need(v_scale, torch.float32, "v_scale", shape=k_cache.shape[:3])
-    return k_cache.shape
+        _need(k_scale, torch.float32, "k_scale", shape=shape[:3])
+        _need(v_scale, torch.float32, "v_scale", shape=shape[:3])
+    return shape
+
+
+def _one_device(names, *operands):
+    """_on_device for operands given in the order of `names`; returns the index
+    of the device and its current stream's handle."""
+    at = operands[0].get_device()
+    if at < 0 or at != torch.cuda.current_device() or any(t is not None and t.get_device() != at for t in operands):
+        _on_device(**dict(zip(names.split(), operands)))
+    return at, torch.cuda.current_stream(at).cuda_stream
+
+
+def _at(t: Optional[torch.Tensor]):
+    return None if t is None else t.data_ptr()
 
 
 def convrot_rope_append(q, k, v, rope, positions, slots, k_cache, v_cache, *, k_scale=None, v_scale=None,
@@ -465,31 +487,30 @@ def convrot_rope_append(q, k, v, rope, positions, slots, k_cache, v_cache, *, k_
     (page * page_size + offset; negative: nowhere).  Returns (q_out, k_out);
     the rotated k is written only where the caller gives a k_out.  q_out and
     k_out may be q and k themselves."""
-    T, Hq, D = _heads(q, "q")
-    Hkv = _heads(k, "k", T, None, D)[1]
-    _heads(v, "v", T, Hkv, D)
-    pages, _, page_size, _ = _cache(k_cache, v_cache, k_scale, v_scale)
-    if k_cache.shape[1] != Hkv or k_cache.shape[3] != D:
+    T, Hq, D, sq = _heads(q, "q")
+    _, Hkv, _, sk = _heads(k, "k", T, None, D)
+    sv = _heads(v, "v", T, Hkv, D)[3]
+    pages, heads, page_size, dim = _cache(k_cache, v_cache, k_scale, v_scale)
+    if heads != Hkv or dim != D:
         raise ValueError(f"k_cache must hold {Hkv} heads of {D} elements, got shape {tuple(k_cache.shape)}")
     _need(rope, torch.float32, "rope", 2)
-    _need(positions, torch.int32, "positions", shape=(T,))
-    _need(slots, torch.int64, "slots", shape=(T,))
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _need(w, torch.float32, name, shape=(D,))
-    if q_out is not None:
-        _heads(q_out, "q_out", T, Hq, D)
-    if k_out is not None:
-        _heads(k_out, "k_out", T, Hkv, D)
-    dev = _on_device(q=q, k=k, v=v, rope=rope, positions=positions, slots=slots, k_cache=k_cache, v_cache=v_cache,
-                     k_scale=k_scale, v_scale=v_scale, q_norm=q_norm, k_norm=k_norm, q_out=q_out, k_out=k_out)
+    _vector(positions, torch.int32, "positions", T)
+    _vector(slots, torch.int64, "slots", T)
+    if q_norm is not None:
+        _vector(q_norm, torch.float32, "q_norm", D)
+    if k_norm is not None:
+        _vector(k_norm, torch.float32, "k_norm", D)
+    sqo = sq if q_out is q else _heads(q_out, "q_out", T, Hq, D)[3] if q_out is not None else Hq * D
+    sko = _heads(k_out, "k_out", T, Hkv, D)[3] if k_out is not None else 0
+    dev, stream = _one_device("q k v rope positions slots k_cache v_cache k_scale v_scale q_norm k_norm q_out k_out", q, k, v,
+                              rope, positions, slots, k_cache, v_cache, k_scale, v_scale, q_norm, k_norm, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+    R, turned = rope.shape
     _check("convrot_rope_append", lib().convrot_rope_append(
-        _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), T, Hq, Hkv, D, _ptr(rope),
-        rope.shape[0], rope.shape[1], _ptr(positions), _ptr(slots), _ptr(q_norm), _ptr(k_norm), eps, _ptr(q_out),
-        _row_stride(q_out), _ptr(k_out), 0 if k_out is None else _row_stride(k_out), _ptr(k_cache), _ptr(v_cache),
-        _ptr(k_scale), _ptr(v_scale), pages, page_size, _stream(dev)))
+        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, Hq, Hkv, D, rope.data_ptr(), R, turned, positions.data_ptr(),
+        slots.data_ptr(), _at(q_norm), _at(k_norm), eps, q_out.data_ptr(), sqo, _at(k_out), sko, k_cache.data_ptr(),
+        v_cache.data_ptr(), _at(k_scale), _at(v_scale), pages, page_size, stream))
     return q_out, k_out
 
 
@@ -499,27 +520,26 @@ def convrot_attention_prompt(q, k, v, cu_seqlens, cu_seqlens_k=None, *, scale: O
     cu_seqlens[i] .. cu_seqlens[i + 1] of q, and of k and v unless they have
     offsets of their own.  scale None: D ** -0.5.  A new `out` is not
     initialised: rows of no sequence hold what the memory held."""
-    T, Hq, D = _heads(q, "q")
-    Tk, Hkv, _ = _heads(k, "k", None, None, D)
-    _heads(v, "v", Tk, Hkv, D)
+    T, Hq, D, sq = _heads(q, "q")
+    Tk, Hkv, _, sk = _heads(k, "k", None, None, D)
+    sv = _heads(v, "v", Tk, Hkv, D)[3]
     _need(cu_seqlens, torch.int32, "cu_seqlens", 1)
+    n = cu_seqlens.shape[0] - 1
     if cu_seqlens_k is None:
         if Tk != T:
             raise ValueError("k and q have different lengths: cu_seqlens_k is needed")
         cu_seqlens_k = cu_seqlens
     else:
-        _need(cu_seqlens_k, torch.int32, "cu_seqlens_k", shape=cu_seqlens.shape)
-    if cu_seqlens.numel() < 1:
+        _vector(cu_seqlens_k, torch.int32, "cu_seqlens_k", n + 1)
+    if n < 0:
         raise ValueError("cu_seqlens must hold one offset more than there are sequences")
-    if out is not None:
-        _heads(out, "out", T, Hq, D)
-    dev = _on_device(q=q, k=k, v=v, cu_seqlens=cu_seqlens, cu_seqlens_k=cu_seqlens_k, out=out)
+    so = _heads(out, "out", T, Hq, D)[3] if out is not None else Hq * D
+    dev, stream = _one_device("q k v cu_seqlens cu_seqlens_k out", q, k, v, cu_seqlens, cu_seqlens_k, out)
     if out is None:
-        out = torch.empty(T, Hq, D, dtype=torch.bfloat16, device=dev)
+        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
     _check("convrot_attention_prompt", lib().convrot_attention_prompt(
-        _ptr(q), _row_stride(q), _ptr(k), _row_stride(k), _ptr(v), _row_stride(v), T, Tk, Hq, Hkv, D, _ptr(cu_seqlens),
-        _ptr(cu_seqlens_k), cu_seqlens.numel() - 1, D ** -0.5 if scale is None else scale, int(causal), _ptr(out),
-        _row_stride(out), _stream(dev)))
+        q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, Tk, Hq, Hkv, D, cu_seqlens.data_ptr(),
+        cu_seqlens_k.data_ptr(), n, D ** -0.5 if scale is None else scale, int(causal), out.data_ptr(), so, stream))
     return out
 
 
@@ -532,31 +552,33 @@ def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_sc
     """Attention of one new token per sequence over a paged cache (bf16, or
     int8 with scales).  seq_lens counts the new token, whose key and value the
     cache already holds.  scale None: D ** -0.5."""
-    B, Hq, D = _heads(q, "q")
+    B, Hq, D, sq = _heads(q, "q")
     pages, Hkv, page_size, Dc = _cache(k_cache, v_cache, k_scale, v_scale)
     if Dc != D:
         raise ValueError(f"q has {D} elements per head, the cache {Dc}")
-    if not isinstance(block_table, torch.Tensor) or block_table.dtype != torch.int32:
+    if not isinstance(block_table, torch.Tensor) or block_table.dtype is not torch.int32:
         raise TypeError("block_table must be a torch.int32 tensor")
     if block_table.dim() != 2 or block_table.shape[0] != B:
         raise ValueError(f"block_table must have shape ({B}, pages per sequence), got {tuple(block_table.shape)}")
     cols = block_table.shape[1]
-    if block_table.numel() and ((cols > 1 and block_table.stride(1) != 1) or (B > 1 and block_table.stride(0) < cols)):
+    st, sc = block_table.stride()
+    if ((cols > 1 and sc != 1) or (B > 1 and st < cols)) and block_table.numel():
         raise ValueError("block_table must have contiguous rows")
-    _need(seq_lens, torch.int32, "seq_lens", shape=(B,))
-    if out is not None:
-        _heads(out, "out", B, Hq, D)
-    dev = _on_device(q=q, k_cache=k_cache, v_cache=v_cache, block_table=block_table, seq_lens=seq_lens,
-                     k_scale=k_scale, v_scale=v_scale, out=out)
+    _vector(seq_lens, torch.int32, "seq_lens", B)
+    so = _heads(out, "out", B, Hq, D)[3] if out is not None else Hq * D
+    dev, stream = _one_device("q k_cache v_cache block_table seq_lens k_scale v_scale out", q, k_cache, v_cache, block_table,
+                              seq_lens, k_scale, v_scale, out)
     if out is None:
-        out = torch.empty(B, Hq, D, dtype=torch.bfloat16, device=dev)
-    if workspace is None and torch.cuda.is_current_stream_capturing():
-        workspace = Workspace(dev.index)  # a graph's own: graphs may be replayed at the same time
-    ws, wn = _workspace(dev, convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D), workspace)
+        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+    if workspace is None:
+        # a captured graph gets its own: graphs may be replayed at the same time
+        workspace = (Workspace(dev) if torch.cuda.is_current_stream_capturing() else
+                     _default_ws.get((dev, stream)) or _default_ws.setdefault((dev, stream), Workspace(dev)))
+    ws, wn = workspace.get(convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D))
     _check("convrot_attention_decode", lib().convrot_attention_decode(
-        _ptr(q), _row_stride(q), B, Hq, Hkv, D, _ptr(k_cache), _ptr(v_cache), _ptr(k_scale), _ptr(v_scale), pages,
-        page_size, _ptr(block_table), max(cols, block_table.stride(0)) if B > 1 else cols, cols, _ptr(seq_lens),
-        D ** -0.5 if scale is None else scale, _ptr(out), _row_stride(out), ws, wn, _stream(dev)))
+        q.data_ptr(), sq, B, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), pages, page_size,
+        block_table.data_ptr(), st if B > 1 else cols, cols, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,
+        out.data_ptr(), so, ws, wn, stream))
     return out
 
 

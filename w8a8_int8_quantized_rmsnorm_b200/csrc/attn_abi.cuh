@@ -60,10 +60,13 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   a.head_chunks = (group + 127) / 128;
   a.tile_heads = (group + a.head_chunks - 1) / a.head_chunks;
   a.tile_tokens = 128 / a.tile_heads;
-  CUtensorMap mq, mk, mv;
+  a.boxed = 32 % a.tile_heads == 0;
+  CUtensorMap mq, mk, mv, mo;
   if (!make_heads_map(&mq, a.q, a.tokens, a.q_heads, D, a.q_stride, a.tile_heads, a.tile_tokens))
     return CONVROT_ERR_CUDA;
-  mk = mv = mq;  // without keys nothing is fetched through them
+  mk = mv = mo = mq;  // without keys nothing is fetched through them
+  if (a.boxed && !make_heads_map(&mo, a.o, a.tokens, a.q_heads, D, a.o_stride, a.tile_heads, 32 / a.tile_heads))
+    return CONVROT_ERR_CUDA;
   if (a.kv_tokens > 0 && (!make_heads_map(&mk, a.k, a.kv_tokens, a.kv_heads, D, a.k_stride, 1, PROMPT_KEYS) ||
                           !make_heads_map(&mv, a.v, a.kv_tokens, a.kv_heads, D, a.v_stride, 1, PROMPT_KEYS)))
     return CONVROT_ERR_CUDA;
@@ -79,7 +82,7 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   const int64_t units = (static_cast<int64_t>(a.tokens) / (2 * a.tile_tokens) + std::min(a.seqs, a.tokens)) *
                         a.kv_heads * a.head_chunks;
   const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, d.sms));
-  return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, a);
+  return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, mo, a);
 }
 
 // Heads of a decode unit: up to eight together, else sixteen at a time.

@@ -45,6 +45,7 @@ struct PromptArgs {
   int head_chunks;                                 // tiles side by side for one group
   float scale_log2;                                // scale * log2(e)
   int causal;
+  int boxed;                                       // a warp's 32 rows are whole tokens: tile_heads divides 32
 };
 
 constexpr int PROMPT_KEYS = 128;     // keys per tile
@@ -61,7 +62,7 @@ struct PromptSmem {
   // us with; with D = 128 the tensor core does, and nothing was gained.
   static constexpr int POLY = D == 128 ? 1 << 20 : 4;
   static constexpr int RING = 2 * TILE;
-  static constexpr int OUT = RING + STAGES * TILE;        // 4 KB per softmax warp: 32 rows of 64 elements
+  static constexpr int OUT = RING + STAGES * TILE;        // a softmax warp's 32 result rows, 64 elements after 64
   static constexpr int BARS = OUT + 8 * 4096;
   static constexpr int N_BARS = 2 * STAGES + 17;
   static constexpr int INFO = BARS + 8 * N_BARS;
@@ -136,6 +137,14 @@ __device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
       : "memory");
 }
 constexpr uint32_t IDESC_B_MN_MAJOR = 1u << 16;
+
+// 3-D tiled store shared -> global (bulk-group completion).
+__device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void* src, int c0, int c1, int c2) {
+  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                   reinterpret_cast<uint64_t>(map)),
+               "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
+               : "memory");
+}
 
 // True in one lane of a converged warp, the same one every time.
 __device__ __forceinline__ bool elect_one() {
@@ -271,7 +280,7 @@ __device__ __forceinline__ int prompt_limit(const PromptUnit& u, int causal, int
 template <int D>
 __global__ void __launch_bounds__(PROMPT_THREADS, 1)
 prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
-              const __grid_constant__ CUtensorMap tm_v, const PromptArgs a) {
+              const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_o, const PromptArgs a) {
   using SM = PromptSmem<D>;
   constexpr int S = SM::STAGES;
   constexpr int HALVES = D / 64;         // 128-byte lines per row
@@ -316,6 +325,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       tma_prefetch_desc(&tm_q);
       tma_prefetch_desc(&tm_k);
       tma_prefetch_desc(&tm_v);
+      tma_prefetch_desc(&tm_o);
     }
   }
   tc_fence_before();
@@ -637,55 +647,83 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       if (!ok) break;
       // ---- result
       // A thread holds a row; stored as they are, 32 rows at a time, the pieces
-      // of a warp's store would lie in 32 lines.  So the warp turns 64 elements of
-      // its rows at a time in shared memory and stores whole 128-byte lines.
-      const uint32_t out_off = static_cast<uint32_t>(i) * static_cast<uint32_t>(a.o_stride / 8) + hd * (D / 8);  // 16-byte pieces
-      uint16_t* out = a.o + static_cast<int64_t>(u.tok0) * a.o_stride + static_cast<int64_t>(u.head0) * D;
+      // of a warp's store would lie in 32 lines, and the softmax would wait for
+      // the stores.  So the warp lays its rows out in shared memory and one TMA
+      // store takes them while the next unit runs.  A box cannot end between
+      // tokens of two sequences: the last rows of a sequence, and groups that
+      // do not divide 32, are stored from there in whole 128-byte lines.
       const unsigned stored = __ballot_sync(0xFFFFFFFFu, valid);
-      bool bad = false;
+      const bool boxed = a.boxed && stored == 0xFFFFFFFFu;
+      uint64_t nan2 = 0;
       if (n_tiles > 0) {
         if (!prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
         tc_fence_after();
       }
       const float inv = lim > 0 ? 1.f / l : 0.f;
-      const uint32_t mine = smem_addr(smem + SM::OUT + warp * 4096);
+      const uint64_t inv2 = pack2(inv, inv);
+      uint8_t* lines = smem + SM::OUT + warp * 4096;
+      const uint32_t mine = smem_addr(lines);
+      const uint32_t out_off = static_cast<uint32_t>(i) * static_cast<uint32_t>(a.o_stride / 8) + hd * (D / 8);  // 16-byte pieces
 #pragma unroll
-      for (int x = 0; x < D / 64; ++x) {
+      for (int x = 0; x < D / 64; ++x) {  // 64 elements of every row
+        if (lane == 0) bulk_wait_group_read<0>();  // the store before this one has left shared memory
+        __syncwarp();
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t o[16];
+        for (int y = 0; y < 2; ++y) {
+          uint32_t o[32];
           if (n_tiles > 0) {
-            tmem_ld_x16(t_o + 64 * x + 16 * y, o);
+            tmem_ld_32x32b_x32(t_o + 64 * x + 32 * y, o);
             tmem_ld_wait();
           }
+          if (lim == 0) {  // sees nothing: zero, whatever the accumulator holds
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = 0;
+          }
+          uint32_t r[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {
-            const float f = n_tiles > 0 && lim > 0 ? __uint_as_float(o[e]) * inv : 0.f;
-            bad |= f != f;
-            o[e] = __float_as_uint(f);
+            float lo, hi;
+            const uint64_t f = mul2(pack2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2);
+            nan2 = add2(nan2, f);
+            unpack2(f, lo, hi);
+            r[e] = cvt_bf16x2(lo, hi);
           }
 #pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            uint32_t r[4];
+          for (int e = 0; e < 4; ++e)
+            sts128(mine + lane * 128 + (((4 * y + e) ^ (lane & 7)) << 4), r[4 * e], r[4 * e + 1], r[4 * e + 2], r[4 * e + 3]);
+        }
+        if (boxed) {
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_3d(&tm_o, lines, 64 * x, u.head0, u.tok0 + i);
+            bulk_commit_group();
+          }
+        } else {
+          __syncwarp();
+          uint16_t* out = a.o + static_cast<int64_t>(u.tok0) * a.o_stride + static_cast<int64_t>(u.head0) * D;
 #pragma unroll
-            for (int z = 0; z < 4; ++z) r[z] = cvt_bf16x2(__uint_as_float(o[8 * e + 2 * z]), __uint_as_float(o[8 * e + 2 * z + 1]));
-            sts128(mine + lane * 128 + (((2 * y + e) ^ (lane & 7)) << 4), r[0], r[1], r[2], r[3]);
+          for (int y = 0; y < 8; ++y) {  // four rows at a time, eight lanes a row
+            const int r = 4 * y + (lane >> 3);
+            const uint4 v = lds128(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+            const uint32_t off = __shfl_sync(0xFFFFFFFFu, out_off, r);
+            if ((stored >> r) & 1u) *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(off) + 8 * x + (lane & 7)) * 8) = v;
           }
         }
-        __syncwarp();
-#pragma unroll
-        for (int y = 0; y < 8; ++y) {  // four rows at a time, eight lanes a row
-          const int r = 4 * y + (lane >> 3);
-          const uint4 v = lds128(mine + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
-          const uint32_t off = __shfl_sync(0xFFFFFFFFu, out_off, r);
-          if ((stored >> r) & 1u) *reinterpret_cast<uint4*>(out + (static_cast<int64_t>(off) + 8 * x + (lane & 7)) * 8) = v;
-        }
-        __syncwarp();
       }
       if (n_tiles > 0) tc_fence_before();
+      // a sum of results is a NaN if one of them is (or if two are opposite
+      // infinities: that row is then computed twice, to the same end)
+      float n0, n1;
+      unpack2(nan2, n0, n1);
+      const bool bad = lim > 0 && n0 + n1 != n0 + n1;
       unsigned again = __ballot_sync(0xFFFFFFFFu, bad && valid);
       if (again) {
-        if (lane == 0) atomicAdd(const_cast<int*>(busy), 1);
+        if (lane == 0) {
+          atomicAdd(const_cast<int*>(busy), 1);
+          bulk_wait_group<0>();  // the rows are stored before they are stored again
+        }
+        __syncwarp();
         while (again) {
           const int r = __ffs(again) - 1;
           again &= again - 1;
@@ -702,6 +740,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       __syncwarp();
       if (lane == 0) mbar_arrive(&info_empty[n_info & 1u]);
     }
+    if (lane == 0) bulk_wait_group<0>();
   }
   __syncthreads();
   if (warp == 8) tmem_dealloc(tmem, 512);

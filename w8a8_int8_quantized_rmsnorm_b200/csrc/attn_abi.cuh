@@ -81,7 +81,8 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   // the lengths are on the device: at most this many units
   const int64_t units = (static_cast<int64_t>(a.tokens) / (2 * a.tile_tokens) + std::min(a.seqs, a.tokens)) *
                         a.kv_heads * a.head_chunks;
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(units, d.sms));
+  if (units > 0x7FFFFFFF) return CONVROT_ERR_SHAPE;
+  const unsigned grid = static_cast<unsigned>(units);
   return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, mo, a);
 }
 

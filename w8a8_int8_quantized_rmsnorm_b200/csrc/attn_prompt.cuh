@@ -14,9 +14,12 @@
 //
 // Work split.  A unit is 2 x 128 query rows of one key/value head: a row is
 // (token, query head of the group), so a group's heads share every key and
-// value tile and a short prompt still fills the matrix unit.  A persistent CTA
-// per SM takes units by a fixed order, the longest key ranges first and every
-// second round backwards.  Warps 0-3 and 4-7 each own one 128-row tile (a
+// value tile and a short prompt still fills the matrix unit.  The grid has one
+// CTA per unit, the longest key ranges first; one runs per SM, and when a unit's
+// last copies are under way it takes over the next unit that has not started
+// (clusterlaunchcontrol.try_cancel) instead of ending: a pack of very different
+// lengths spreads evenly, and set-up, fetch and store of neighbouring units
+// overlap.  Warps 0-3 and 4-7 each own one 128-row tile (a
 // thread owns a row; no exchange between threads), warp 8 fetches by TMA and
 // announces units, warp 9 issues the matrix products.  While one tile's
 // softmax runs, the tensor core works on the other's S or O.
@@ -64,10 +67,11 @@ struct PromptSmem {
   static constexpr int RING = 2 * TILE;
   static constexpr int OUT = RING + STAGES * TILE;        // a softmax warp's 32 result rows, 64 elements after 64
   static constexpr int BARS = OUT + 8 * 4096;
-  static constexpr int N_BARS = 2 * STAGES + 17;
+  static constexpr int N_BARS = 2 * STAGES + 18;
   static constexpr int INFO = BARS + 8 * N_BARS;
   static constexpr int MISC = INFO + 2 * 48;
-  static constexpr int TOTAL = MISC + 16 + 1024;          // + alignment of the first tile
+  static constexpr int TAKE = (MISC + 16 + 15) / 16 * 16; // two 16-byte answers to try_cancel
+  static constexpr int TOTAL = TAKE + 32 + 1024;          // + alignment of the first tile
 };
 
 // One unit of work as the fetching warp announces it.
@@ -144,6 +148,28 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, const void*
                    reinterpret_cast<uint64_t>(map)),
                "r"(smem_addr(src)), "r"(c0), "r"(c1), "r"(c2)
                : "memory");
+}
+
+// Asks for the next CTA of the grid that has not started; the 16-byte answer
+// completes on `bar`.
+__device__ __forceinline__ void take_next(uint32_t answer, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(answer),
+               "r"(smem_addr(bar))
+               : "memory");
+}
+// The index of the CTA taken over, or -1 if every one has started.
+__device__ __forceinline__ int taken_index(uint32_t answer) {
+  uint32_t x, got;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
+      "ld.shared.b128 r, [%2];\n\t"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n\t"
+      "selp.u32 %1, 1, 0, p;\n\tmov.u32 %0, 0;\n\t"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, r;\n\t}"
+      : "=r"(x), "=r"(got)
+      : "r"(answer)
+      : "memory");
+  return got ? static_cast<int>(x) : -1;
 }
 
 // True in one lane of a converged warp, the same one every time.
@@ -290,7 +316,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + SM::BARS);
   uint64_t *kv_full = bars, *kv_empty = bars + S, *q_full = bars + 2 * S, *q_empty = q_full + 2,
            *s_full = q_full + 4, *p_full = q_full + 6, *o_done = q_full + 8, *info_full = q_full + 10,
-           *info_empty = q_full + 12, *drain = q_full + 14, *p_rest = q_full + 15;
+           *info_empty = q_full + 12, *drain = q_full + 14, *p_rest = q_full + 15, *taken = q_full + 17;
   PromptUnit* info = reinterpret_cast<PromptUnit*>(smem + SM::INFO);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + SM::MISC);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -314,6 +340,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       mbar_init(&info_empty[i], 9);  // the issuing warp and the eight softmax warps
     }
     mbar_init(drain, 1);
+    mbar_init(taken, 1);
     *abort_flag = 0;
     *busy = 0;
     fence_barrier_init();
@@ -353,10 +380,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const int group = a.q_heads / a.kv_heads;
       uint32_t it = 0, q_use[2] = {0, 0}, n_info = 0;
       bool ok = true;
-      for (int64_t round = 0; ok; ++round) {
-        const int64_t at = round * gridDim.x + ((round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
-        if (at >= units && round * gridDim.x >= units) break;
-        if (at >= units) continue;
+      const uint32_t answer = smem_addr(smem + SM::TAKE);
+      uint32_t asked = 0;
+      for (int64_t at = blockIdx.x; ok && at >= 0;) {
+        if (at < units) {
         // the blocks with the most keys first, a block's heads side by side
         const int block = total - 1 - static_cast<int>(at / heads);
         const int head = static_cast<int>(at % heads);
@@ -425,7 +452,22 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           }
         }
         ++n_info;
+        }
+        // (asked only now: whoever asks early keeps others from a fair share)
+        if (lane == 0 && ok) {
+          mbar_arrive_expect_tx(taken, 16);
+          take_next(answer + 16 * (asked & 1u), taken);
+          ok = prompt_wait(taken, asked & 1u, abort_flag, busy, SITE_ATTN);
+          if (!ok) {  // its answer may not land after the CTA has gone
+            int never = 0;
+            mbar_wait(taken, asked & 1u, &never, SITE_DRAIN);
+          }
+        }
         ok = __shfl_sync(0xFFFFFFFFu, static_cast<int>(ok), 0) != 0;
+        at = ok ? taken_index(answer + 16 * (asked & 1u)) : -1;
+        fence_proxy_async_smem();  // this answer is read before a later one is written
+        __syncwarp();
+        ++asked;
       }
       if (lane == 0) {
         if (ok && prompt_wait(&info_empty[n_info & 1u], ((n_info >> 1) & 1u) ^ 1u, abort_flag, busy, SITE_ATTN)) {

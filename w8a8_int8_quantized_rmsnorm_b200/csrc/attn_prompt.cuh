@@ -613,6 +613,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         ok = prompt_wait(&s_full[w], s_use & 1u, abort_flag, busy, SITE_ATTN + 4);
         if (!ok) break;
         tc_fence_after();
+        const bool whole = 2 * j + 2 <= n_halves;  // else half a tile; the same for the whole warpgroup
         uint32_t s[4][32];
 #pragma unroll
         for (int x = 0; x < 4; ++x) tmem_ld_32x32b_x32(t_s + 32 * x, s[x]);
@@ -621,17 +622,28 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           const int rel = lim - j * PROMPT_KEYS, warp_rel = warp_lim - j * PROMPT_KEYS;
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            if (32 * (x + 1) > warp_rel) {
+            if (32 * (x + 1) > warp_rel && (x < 2 || whole)) {
+              // one bit per key that is seen
+              const int seen = min(32, max(0, rel - 32 * x));
+              const uint32_t bits = seen < 32 ? (1u << seen) - 1u : 0xFFFFFFFFu;
 #pragma unroll
               for (int e = 0; e < 32; ++e)
-                if (32 * x + e >= rel) s[x][e] = 0xFF800000u;  // -inf
+                if (!(bits & (1u << e))) s[x][e] = 0xFF800000u;  // -inf
             }
         }
         float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
+        for (int e = 0; e < 32; e += 4)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) top[x] = max3(top[x], __uint_as_float(s[x][e]), __uint_as_float(s[x][e + 1]));
+          for (int x = 0; x < 4; ++x)
+            top[x] = max3(top[x], __uint_as_float(s[x / 2][e + 2 * (x % 2)]), __uint_as_float(s[x / 2][e + 2 * (x % 2) + 1]));
+        if (whole) {
+#pragma unroll
+          for (int e = 0; e < 32; e += 4)
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+              top[x] = max3(top[x], __uint_as_float(s[2 + x / 2][e + 2 * (x % 2)]), __uint_as_float(s[2 + x / 2][e + 2 * (x % 2) + 1]));
+        }
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
         if (j == 0) {
           m = high;
@@ -658,7 +670,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
         uint64_t sum2[2] = {0, 0};
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          if (x >= 2 && 2 * j + 2 > n_halves) break;  // the same for the whole warpgroup
+          if (x >= 2 && !whole) break;
           uint32_t p[16];
 #pragma unroll
           for (int e = 0; e < 16; ++e) {

@@ -301,6 +301,7 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_counter_bytes(grid));
   // no more CTAs than blocks there can be
   const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + DECODE_KEYS - 1) / DECODE_KEYS);
+  if (most > 0x7FFFFFFF / (static_cast<int64_t>(seqs) * kv_heads * a.chunks)) return CONVROT_ERR_UNSUPPORTED;
   const int64_t blocks = most * seqs * kv_heads * a.chunks;
   const bool i8 = k_scale != nullptr;
   const int h = a.chunk_heads;

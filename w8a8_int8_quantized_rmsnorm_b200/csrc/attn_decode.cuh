@@ -68,12 +68,14 @@ __host__ __device__ constexpr int decode_part_floats(int heads, int D) { return 
 
 // What a ring slot holds besides keys and values.
 struct DecodeBlock {
-  int seq, unit;        // unit: (kv head, head chunk); seq < 0: no more blocks
   int left;             // keys of the sequence from the block's first one on
-  unsigned slices;      // 16-key slices that are there
-  int first, last;      // begins / ends this CTA's stretch of the (seq, unit)
+  unsigned flags;       // bits 0-3: the 16-key slices that are there; then:
+  int seq, unit;        // unit: (kv head, head chunk)
   int owner, n_parts;   // CTA of the (seq, unit)'s first block; parts (1: whole)
+  int pad[2];
 };
+// begins / ends this CTA's stretch of the (seq, unit); no more blocks
+constexpr unsigned BLOCK_FIRST = 16, BLOCK_LAST = 32, BLOCK_END = 64;
 
 template <int D, bool I8, int NQ>
 struct DecodeSmem {
@@ -192,11 +194,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   __syncthreads();
   pdl_wait();
 
-  const int units = a.kv_heads * a.chunks;
+  const unsigned units = a.kv_heads * a.chunks;
   if (warp == 4) {
     // -------------------------------------------------------- fetch
     // this CTA's stretch [begin, end) of the line of blocks
-    int64_t total = 0;
+    unsigned total = 0;  // the host has seen that line indices fit in 31 bits
     for (int b0 = lane; b0 < a.seqs; b0 += 128) {
       int n = 0;
 #pragma unroll
@@ -207,7 +209,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
     for (int o = 16; o; o >>= 1) total += __shfl_xor_sync(0xFFFFFFFFu, total, o);
     total *= units;
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, begin = per * blockIdx.x, end = min(total, begin + per);
+    const unsigned per = (total + gridDim.x - 1) / gridDim.x, begin = min(total, per * blockIdx.x), end = min(total, begin + per);
 
     // A batch: consecutive blocks of one (sequence, unit), as many as a warp's
     // lanes can hold the pages of, so that the block table's latency is paid
@@ -215,7 +217,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     const int boxes = DECODE_KEYS / a.box_rows, most = 32 / boxes;
     const unsigned page_size = a.page_size;
     struct Batch {
-      int64_t at, start;  // line index of the batch, and of the sequence's first block
+      unsigned at, start;  // line index of the batch, and of the sequence's first block
       int seq, unit, len, nb, j, n;
     } cur = {begin, 0, 0, 0, 0, 1, 0, 0}, next;
     if (begin < end) {
@@ -228,22 +230,22 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           const int up = __shfl_up_sync(0xFFFFFFFFu, sum, o);
           if (lane >= o) sum += up;
         }
-        const unsigned hit = __ballot_sync(0xFFFFFFFFu, cur.start + static_cast<int64_t>(sum) * units > begin);
+        const unsigned hit = __ballot_sync(0xFFFFFFFFu, cur.start + static_cast<unsigned>(sum) * units > begin);
         if (hit) {
           const int l = __ffs(hit) - 1;
           cur.seq = b0 + l;
           cur.len = __shfl_sync(0xFFFFFFFFu, ln, l);
           cur.nb = decode_blocks(cur.len);
-          cur.start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, l) - cur.nb) * units;
+          cur.start += static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, sum, l) - cur.nb) * units;
           break;
         }
-        cur.start += static_cast<int64_t>(__shfl_sync(0xFFFFFFFFu, sum, 31)) * units;
+        cur.start += static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, sum, 31)) * units;
       }
-      cur.unit = static_cast<int>((begin - cur.start) / cur.nb);
-      cur.j = static_cast<int>((begin - cur.start) - static_cast<int64_t>(cur.unit) * cur.nb);
+      cur.unit = static_cast<int>((begin - cur.start) / static_cast<unsigned>(cur.nb));
+      cur.j = static_cast<int>(begin - cur.start) - cur.unit * cur.nb;
     }
     auto size = [&](const Batch& b) {
-      return static_cast<int>(min(static_cast<int64_t>(min(most, b.nb - b.j)), end - b.at));
+      return min(min(most, b.nb - b.j), static_cast<int>(end - b.at));
     };
     // page of this lane's box of the batch; -1: not there
     auto pages_of = [&](const Batch& b) -> int {
@@ -264,10 +266,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       next.j += cur.n;
       if (next.j == cur.nb) {
         next.j = 0;
-        if (++next.unit == units) {
+        if (++next.unit == static_cast<int>(units)) {
           next.unit = 0;
           ++next.seq;
-          next.start += static_cast<int64_t>(cur.nb) * units;
+          next.start += static_cast<unsigned>(cur.nb) * units;
           next.len = next_len;
           next.nb = decode_blocks(next_len);
         }
@@ -281,7 +283,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       }
       const int kvh = cur.unit / a.chunks, chunk = cur.unit - kvh * a.chunks;
       const int qh = min(heads, group - chunk * heads);
-      const int64_t item = cur.start + static_cast<int64_t>(cur.unit) * cur.nb;
+      const unsigned item = cur.start + static_cast<unsigned>(cur.unit) * cur.nb;
       for (int i = 0; i < cur.n; ++i) {
         ok = mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
         if (!ok) break;
@@ -299,10 +301,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           m.seq = cur.seq;
           m.unit = cur.unit;
           m.left = cur.len - j * DECODE_KEYS;
-          m.slices = 0;
-          for (int x = 0; x < 4; ++x) m.slices |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
-          m.first = first;
-          m.last = last;
+          m.flags = (first ? BLOCK_FIRST : 0) | (last ? BLOCK_LAST : 0);
+          for (int x = 0; x < 4; ++x) m.flags |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
+          m.pad[0] = m.pad[1] = 0;
           m.owner = blockIdx.x;
           m.n_parts = 1;
           if (last && (item < begin || item + cur.nb > end)) {  // twice per CTA at most: its two ends
@@ -337,7 +338,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     }
     ok = ok && mbar_wait_spin(&empty[s], phase, abort_flag, SITE_DECODE);
     if (ok && lane == 0) {
-      meta[s].seq = -1;
+      meta[s].flags = BLOCK_END;
       mbar_arrive(&full[s]);
     }
     // No copy may still be landing in shared memory when the CTA exits.  The
@@ -377,9 +378,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       const uint32_t s = next;
       if (!mbar_wait_spin(&full[s], phase, abort_flag, SITE_DECODE + 2)) break;
       if (++next == static_cast<uint32_t>(S)) next = 0, phase ^= 1u;
-      const DecodeBlock b = meta[s];
-      if (b.seq < 0) break;
-      if (b.first) {
+      const unsigned flags = meta[s].flags;
+      const int block_left = meta[s].left;
+      if (flags & BLOCK_END) break;
+      if (flags & BLOCK_FIRST) {
         const uint8_t* rows = side + s * SM::SIDE;
         if (I8) {
           // columns 2h and 2h + 1 of a tile: hi and lo of head h; this lane's is column g
@@ -432,8 +434,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
         for (int x = 0; x < HL; ++x) m[x] = -INFINITY, l[x] = 0.f;
       }
-      const int left = b.left - 16 * warp;  // keys of this slice that exist
-      if (left > 0 && ((b.slices >> warp) & 1u)) {
+      const int left = block_left - 16 * warp;  // keys of this slice that exist
+      if (left > 0 && ((flags >> warp) & 1u)) {
         const uint32_t kb = smem_addr(smem + s * SM::SLOT) + slice, vb = kb + SM::TILE;
         float sc[HL][2];  // scores of keys g and g + 8, times log2(e)
         float vs[2] = {1.f, 1.f};
@@ -448,8 +450,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
           const float* scales = reinterpret_cast<const float*>(side + s * SM::SIDE + NQ * D * 2) + 16 * warp + g;
           const float ks[2] = {scales[0] * a.scale_log2, scales[8] * a.scale_log2};
-          vs[0] = g < left ? scales[DECODE_KEYS] : 0.f;
-          vs[1] = g + 8 < left ? scales[DECODE_KEYS + 8] : 0.f;
+          vs[0] = scales[DECODE_KEYS];
+          vs[1] = scales[DECODE_KEYS + 8];
 #pragma unroll
           for (int x = 0; x < HL; ++x)
 #pragma unroll
@@ -470,14 +472,18 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int r = 0; r < 2; ++r) sc[x][r] = (c[x / 2][2 * r + (x & 1)] + d[x / 2][2 * r + (x & 1)]) * a.scale_log2;
         }
+        if (left < 16) {
+#pragma unroll
+          for (int x = 0; x < HL; ++x)
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+              if (g + 8 * r >= left) sc[x][r] = -INFINITY, vs[r] = 0.f;
+        }
         bool high = false;
 #pragma unroll
         for (int x = 0; x < HL; ++x)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
-            if (g + 8 * r >= left) sc[x][r] = -INFINITY;
-            high |= sc[x][r] > m[x] + 8.f;
-          }
+          for (int r = 0; r < 2; ++r) high |= sc[x][r] > m[x] + 8.f;
         if (__any_sync(0xFFFFFFFFu, high)) {
 #pragma unroll
           for (int x = 0; x < HL; ++x) {
@@ -539,9 +545,11 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           }
         }
       }
+      DecodeBlock b;
+      if (flags & BLOCK_LAST) b = meta[s];
       __syncwarp();
       if (lane == 0) mbar_arrive(&empty[s]);
-      if (!b.last) continue;
+      if (!(flags & BLOCK_LAST)) continue;
 
       // ---- join the four warps
       float* st = stat + parity * 4 * NQ * 2;
@@ -621,31 +629,49 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       }
       if (!rendezvous()) break;
       if (!*is_last) continue;
+      // the last part to come joins them all, in the keys' order, eight in flight
+      auto part = [&](int p) {
+        return a.parts + (static_cast<int64_t>(b.owner + p) * 2 + (p == 0 ? 1 : 0)) * part_floats;
+      };
       for (int x = threadIdx.x; x < qh * (D / 4); x += 128) {
         const int h = x / (D / 4), d = (x % (D / 4)) * 4;
         float top = -INFINITY, sum = 0.f;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int p = 0; p < b.n_parts; ++p) {
-          float* part = a.parts + (static_cast<int64_t>(b.owner + p) * 2 + (p == 0 ? 1 : 0)) * part_floats;
-          const float pm = __ldcg(part + heads * D + 2 * h), pl = __ldcg(part + heads * D + 2 * h + 1);
-          const float4 y = __ldcg(reinterpret_cast<const float4*>(part + h * D + d));
-          *reinterpret_cast<float4*>(part + h * D + d) = make_float4(0.f, 0.f, 0.f, 0.f);  // as it was found
-          const float up = fmaxf(top, pm), base = up == -INFINITY ? 0.f : up;
-          const float f = ex2_approx(top - base), fp = ex2_approx(pm - base);
+        for (int p0 = 0; p0 < b.n_parts; p0 += 8) {
+          float2 ml[8];
+          float4 y[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            ml[p] = make_float2(-INFINITY, 0.f);
+            y[p] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p0 + p < b.n_parts) {
+              const float* from = part(p0 + p);
+              ml[p] = __ldcg(reinterpret_cast<const float2*>(from + heads * D) + h);
+              y[p] = __ldcg(reinterpret_cast<const float4*>(from + h * D + d));
+            }
+          }
+          float up = top;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) up = fmaxf(up, ml[p].x);
+          const float base = up == -INFINITY ? 0.f : up, f = ex2_approx(top - base);
           top = up;
-          sum = sum * f + pl * fp;
-          v.x = v.x * f + y.x * fp;
-          v.y = v.y * f + y.y * fp;
-          v.z = v.z * f + y.z * fp;
-          v.w = v.w * f + y.w * fp;
+          sum *= f;
+          v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const float fp = ex2_approx(ml[p].x - base);
+            sum = fmaf(ml[p].y, fp, sum);
+            v.x = fmaf(y[p].x, fp, v.x);
+            v.y = fmaf(y[p].y, fp, v.y);
+            v.z = fmaf(y[p].z, fp, v.z);
+            v.w = fmaf(y[p].w, fp, v.w);
+          }
         }
         store(h, d, v, sum);
       }
       if (!rendezvous()) break;
-      for (int x = threadIdx.x; x < b.n_parts * 2 * qh; x += 128) {
-        const int p = x / (2 * qh);
-        a.parts[(static_cast<int64_t>(b.owner + p) * 2 + (p == 0 ? 1 : 0)) * part_floats + heads * D + x - p * 2 * qh] = 0.f;
-      }
+      for (int x = threadIdx.x; x < b.n_parts * (part_floats / 4); x += 128)  // as it was found
+        reinterpret_cast<float4*>(part(x / (part_floats / 4)))[x % (part_floats / 4)] = make_float4(0.f, 0.f, 0.f, 0.f);
     }
   }
 }

@@ -37,7 +37,7 @@ def norm_rotate(x, weight, table, positions, eps):
     return y, 20 * U * np.concatenate([size, size, np.abs(x[..., 2 * half:])], -1)
 
 
-def attention(q, k, v, scale, visible, q_bits16=False):
+def attention(q, k, v, scale, visible, v_scale=None):
     """One head's rows: q [n, D], k, v [m, D], visible bool [n, m] ->
     (o [n, D], tol [n, D]).
 
@@ -50,9 +50,11 @@ def attention(q, k, v, scale, visible, q_bits16=False):
     * exp2: 2^-12 relative; the probability's rounding: 2^-8;
     * sums of m terms in fp32: m unit roundoffs;
     * the result's rounding: 2^-8 of the result;
-    * q_bits16 (int8 caches): each query element off by half a step of a
-      16-bit grid, max|q| / 32512 / 2, which moves a score by scale * sum |k|
-      times that.
+    * with v_scale [m] (int8 caches, v = code * scale): each query element is
+      off by half a step of a 16-bit grid, max|q| / 32512 / 2, which moves a
+      score by scale * sum |k| times that; each probability times its scale is
+      off by half a step of such a grid of the largest among 32 neighbours,
+      instead of half a step of bf16, which multiplies its key's |code|.
     """
     q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
     n, d = q.shape
@@ -67,10 +69,15 @@ def attention(q, k, v, scale, visible, q_bits16=False):
         p /= p.sum()
         o[i] = p @ v[see]
         ds = 2 * d * U * scale * (np.abs(k[see]) @ np.abs(q[i])).max()
-        if q_bits16:
+        grid = 0.0
+        if v_scale is not None:
             ds += scale * np.abs(q[i]).max() / 65024 * np.abs(k[see]).sum(1).max()
+            w = p * v_scale[see]
+            code = np.abs(v[see]) / np.where(v_scale[see] > 0, v_scale[see], 1)[:, None]
+            for a in range(0, len(see), 32):
+                grid = grid + w[a:a + 32].max() / 65024 * code[a:a + 32].sum(0)
         rel = BF16 + 2.0 ** -12 + 2 * ds + m * U
-        tol[i] = (1 + BF16) * rel * (p @ np.abs(v[see])) + BF16 * np.abs(o[i])
+        tol[i] = (1 + BF16) * (rel * (p @ np.abs(v[see])) + grid) + BF16 * np.abs(o[i])
     return o, tol
 
 
@@ -102,10 +109,13 @@ def paged_attention(q, k_cache, v_cache, k_scale, v_scale, table, lens, scale):
     """One row per sequence: q [B, Hq, D] -> (o, tol)."""
     o, tol = np.zeros(q.shape), np.zeros(q.shape)
     group = q.shape[1] // k_cache.shape[1]
+    page = k_cache.shape[2]
     for b, n in enumerate(lens):
+        at = np.arange(n)
+        s = None if v_scale is None else np.asarray(v_scale, np.float64)[np.asarray(table[b])[at // page], :, at % page]
         k = cache_rows(k_cache, k_scale, table[b], n)
         v = cache_rows(v_cache, v_scale, table[b], n)
         for h in range(q.shape[1]):
             o[b, h], tol[b, h] = (x[0] for x in attention(q[b, h][None], k[:, h // group], v[:, h // group], scale,
-                                                          np.ones((1, n), bool), k_scale is not None))
+                                                          np.ones((1, n), bool), None if s is None else s[:, h // group]))
     return o, tol

@@ -89,7 +89,7 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
 // Heads of a decode unit: up to eight together, else sixteen at a time.
 int decode_unit_heads(int q_heads, int kv_heads) { return std::min(q_heads / kv_heads, 16); }
 
-constexpr int kDecodeCtas = 3;  // most CTAs per SM of any decode kernel
+constexpr int kDecodeCtas = 2;  // most CTAs per SM of any decode kernel
 
 int decode_grid(const DeviceInfo& d) { return kDecodeCtas * d.sms; }
 
@@ -300,7 +300,8 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   a.counters = static_cast<unsigned*>(workspace);
   a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_counter_bytes(grid));
   // no more CTAs than blocks there can be
-  const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + DECODE_KEYS - 1) / DECODE_KEYS);
+  const int keys = k_scale ? DecodeSmem<128, true, 8>::KEYS : DecodeSmem<128, false, 8>::KEYS;
+  const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + keys - 1) / keys);
   if (most > 0x7FFFFFFF / (static_cast<int64_t>(seqs) * kv_heads * a.chunks)) return CONVROT_ERR_UNSUPPORTED;
   const int64_t blocks = most * seqs * kv_heads * a.chunks;
   const bool i8 = k_scale != nullptr;

@@ -1,7 +1,7 @@
 // Attention of one new token per sequence over a paged cache: a stream of
 // every key and value, once, at memory speed.
 //
-// Work split.  The unit of work is a block of 64 keys of one (sequence,
+// Work split.  The unit of work is a block of 64 keys (128 of int8) of one (sequence,
 // key/value head); the heads of its group (up to 8 or 16 at a time) share it.
 // All blocks of the call are laid out in one line, sequence by sequence and
 // head by head, and every CTA takes an equal stretch of the line, so sequences
@@ -13,7 +13,7 @@
 //
 // Inside a CTA one warp fetches (the block table's entries one block ahead,
 // then one TMA box per page piece, into a ring of blocks) and four warps
-// compute, each 16 keys of a block, on warp-level matrix instructions with the
+// compute, each 16 keys of a block (32 of int8), on warp-level matrix instructions with the
 // keys as rows and the heads as columns: S^T = K Q^T and O^T += V^T P^T, so a
 // group of four or eight heads fills the 8-column operand and every score
 // stays with the lane that made it.
@@ -23,14 +23,16 @@
 // rounded to bf16 for the product with V.
 //
 // int8 caches.  Turning codes into bf16 costs 7 instructions per 4 codes, more
-// than the stream leaves time for (both sides converted: 288 us for 128
-// contexts of 1 .. 8192 keys).  So the scores are integer products: a head's
-// query becomes 16-bit fixed point, q = s (256 hi + lo) with s = max|q| / 32512,
-// and hi and lo are two columns of one s8 x s8 -> s32 product with the codes
-// as they are.  The sums are exact; the query is off by at most 2^-16 of its
-// largest element, which moves a score by scale 2^-16 max|q| sum|k| at most,
-// less than the rounding of the probabilities moves the result.  Values become
-// bf16 exactly.  A key's scale multiplies its score, a value's its probability.
+// than the stream leaves time for (both sides converted: 288 us for 128 contexts
+// of 1 .. 8192 keys; the values alone: 215 us).  So both products are integer
+// ones on the codes as they are.  A head's query becomes 16-bit fixed point,
+// q = s (256 hi + lo) with s = max|q| / 32512, and hi and lo are two columns of
+// one s8 x s8 -> s32 product; probabilities times value scales become the same,
+// of the largest among a warp's 32 keys, and their sum joins the fp32 result.
+// The integer sums are exact.  The query is off by at most 2^-16 of its largest
+// element, which moves a score by scale 2^-16 max|q| sum|k| at most; a
+// probability by 2^-16 of the largest beside it, where bf16 would be off by up
+// to 2^-8 of itself.
 //
 // Rows past a sequence's end are never used: their scores are replaced, their
 // values' registers cleared, pages behind the last one not fetched.
@@ -58,7 +60,6 @@ struct DecodeArgs {
   float* parts;                   // [grid][2][decode_part_floats(chunk_heads, D)]
 };
 
-constexpr int DECODE_KEYS = 64;
 constexpr int DECODE_THREADS = 160;
 constexpr unsigned SITE_DECODE = 20;
 constexpr int DECODE_MAX_STAGES = 8;
@@ -69,23 +70,22 @@ __host__ __device__ constexpr int decode_part_floats(int heads, int D) { return 
 // What a ring slot holds besides keys and values.
 struct DecodeBlock {
   int left;             // keys of the sequence from the block's first one on
-  unsigned flags;       // bits 0-3: the 16-key slices that are there; then:
+  unsigned flags;       // bits 0-7: the 16-key slices that are there; then:
   int seq, unit;        // unit: (kv head, head chunk)
   int owner, n_parts;   // CTA of the (seq, unit)'s first block; parts (1: whole)
   int pad[2];
 };
 // begins / ends this CTA's stretch of the (seq, unit); no more blocks
-constexpr unsigned BLOCK_FIRST = 16, BLOCK_LAST = 32, BLOCK_END = 64;
+constexpr unsigned BLOCK_FIRST = 256, BLOCK_LAST = 512, BLOCK_END = 1024;
 
 template <int D, bool I8, int NQ>
 struct DecodeSmem {
   static constexpr int ESZ = I8 ? 1 : 2;
-  // CTAs per SM: two keep enough bf16 rows in flight (64 contexts of 1 .. 8192
-  // keys: 0.98 of HBM); int8 rows need more warps, for the conversions
-  static constexpr int CTAS = I8 && NQ <= 8 ? 3 : 2;
-  static constexpr int TILE = DECODE_KEYS * D * ESZ;
+  static constexpr int CTAS = 2;               // per SM: between them they keep 200 KB in flight
+  static constexpr int KEYS = I8 ? 128 : 64;  // of a block: the same bytes, a multiple of 4 warps x 32 or 16 keys
+  static constexpr int TILE = KEYS * D * ESZ;
   static constexpr int SLOT = 2 * TILE;                            // K, V
-  static constexpr int SIDE = NQ * D * 2 + 2 * DECODE_KEYS * 4;    // Q rows, scales
+  static constexpr int SIDE = NQ * D * 2 + 2 * KEYS * 4;    // Q rows, scales
   static constexpr int PAD = D + 4;                                // floats per joined row
   static int join_bytes(int heads) { return 4 * heads * PAD * 4 + 2 * 4 * NQ * 8 + 2 * NQ * 8; }
   static int total(int stages, int heads) {
@@ -125,13 +125,13 @@ __device__ __forceinline__ void mma_16x8x32(int (&d)[4], const uint32_t (&a)[4],
       : "+r"(d[0]), "+r"(d[1]), "+r"(d[2]), "+r"(d[3])
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
-// Two int8 codes, bytes 0 and 2 of x, as bf16, exactly:
-// (128 + low 7 bits) - (128 or, with the sign bit, 256).
-__device__ __forceinline__ uint32_t codes_to_bf16(uint32_t x) {
-  const uint32_t v = (x & 0x007F007Fu) | 0x43004300u, w = (x & 0x00800080u) | 0x43004300u;
-  uint32_t r;
-  asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(w));
-  return r;
+// d = a * b, the same shapes
+__device__ __forceinline__ void mma_16x8x32_zero(int (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                 uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+      : "=r"(d[0]), "=r"(d[1]), "=r"(d[2]), "=r"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "r"(0));
 }
 __device__ __forceinline__ float ex2_approx(float x) {
   float r;
@@ -154,7 +154,10 @@ __device__ __forceinline__ int decode_length(const DecodeArgs& a, int b) {
   return n;
 }
 // A sequence without keys still has one (empty) block: its result is written.
-__device__ __forceinline__ int decode_blocks(int len) { return max(1, (len + DECODE_KEYS - 1) / DECODE_KEYS); }
+template <int KEYS>
+__device__ __forceinline__ int decode_blocks(int len) {
+  return max(1, static_cast<int>((static_cast<unsigned>(len) + KEYS - 1) / KEYS));
+}
 
 template <int D, bool I8, int NQ>
 __global__ void __launch_bounds__(DECODE_THREADS, DecodeSmem<D, I8, NQ>::CTAS)
@@ -165,6 +168,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
   constexpr int HL = NQ / 4;                           // heads of a lane
   constexpr int NT = (HL + 1) / 2;                     // 8-column tiles of P and O
   constexpr int KS = D / 16;                           // 16-element steps
+  constexpr int KEYS = SM::KEYS, SLICE = KEYS / 4;     // keys of a block, of a warp's share of it
   extern __shared__ uint8_t raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t{1023});
   const int S = a.stages, heads = a.chunk_heads;
@@ -203,7 +207,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       int n = 0;
 #pragma unroll
       for (int x = 0; x < 4; ++x)  // four loads in flight
-        if (b0 + 32 * x < a.seqs) n += decode_blocks(decode_length(a, b0 + 32 * x));
+        if (b0 + 32 * x < a.seqs) n += decode_blocks<KEYS>(decode_length(a, b0 + 32 * x));
       total += n;
     }
 #pragma unroll
@@ -214,7 +218,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     // A batch: consecutive blocks of one (sequence, unit), as many as a warp's
     // lanes can hold the pages of, so that the block table's latency is paid
     // once per batch and behind the one before.
-    const int boxes = DECODE_KEYS / a.box_rows, most = 32 / boxes;
+    const int boxes = KEYS / a.box_rows, most = 32 / boxes;
     const unsigned page_size = a.page_size;
     struct Batch {
       unsigned at, start;  // line index of the batch, and of the sequence's first block
@@ -223,7 +227,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     if (begin < end) {
       for (int b0 = 0;; b0 += 32) {
         const int ln = b0 + lane < a.seqs ? decode_length(a, b0 + lane) : 0;
-        const int n = b0 + lane < a.seqs ? decode_blocks(ln) : 0;
+        const int n = b0 + lane < a.seqs ? decode_blocks<KEYS>(ln) : 0;
         int sum = n;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -235,7 +239,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           const int l = __ffs(hit) - 1;
           cur.seq = b0 + l;
           cur.len = __shfl_sync(0xFFFFFFFFu, ln, l);
-          cur.nb = decode_blocks(cur.len);
+          cur.nb = decode_blocks<KEYS>(cur.len);
           cur.start += static_cast<unsigned>(__shfl_sync(0xFFFFFFFFu, sum, l) - cur.nb) * units;
           break;
         }
@@ -249,7 +253,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     };
     // page of this lane's box of the batch; -1: not there
     auto pages_of = [&](const Batch& b) -> int {
-      const unsigned key = static_cast<unsigned>(b.j) * DECODE_KEYS + lane * a.box_rows;
+      const unsigned key = static_cast<unsigned>(b.j) * KEYS + lane * a.box_rows;
       if (lane >= b.n * boxes || key >= static_cast<unsigned>(b.len)) return -1;
       return a.table[b.seq * a.table_stride + key / page_size];
     };
@@ -271,7 +275,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           ++next.seq;
           next.start += static_cast<unsigned>(cur.nb) * units;
           next.len = next_len;
-          next.nb = decode_blocks(next_len);
+          next.nb = decode_blocks<KEYS>(next_len);
         }
       }
       int page2 = -1;
@@ -289,7 +293,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         if (!ok) break;
         const int j = cur.j + i;
         const int mine = __shfl_sync(0xFFFFFFFFu, page, (i * boxes + lane) & 31);
-        const unsigned key = static_cast<unsigned>(j) * DECODE_KEYS + lane * a.box_rows;  // of this lane's box
+        const unsigned key = static_cast<unsigned>(j) * KEYS + lane * a.box_rows;  // of this lane's box
         const bool wanted = lane < boxes && key < static_cast<unsigned>(cur.len);
         const bool there = wanted && mine >= 0 && mine < a.pages;
         if (wanted && !there) report_error(ERR_BAD_ARGUMENT);
@@ -300,9 +304,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           DecodeBlock m;
           m.seq = cur.seq;
           m.unit = cur.unit;
-          m.left = cur.len - j * DECODE_KEYS;
+          m.left = cur.len - j * KEYS;
           m.flags = (first ? BLOCK_FIRST : 0) | (last ? BLOCK_LAST : 0);
-          for (int x = 0; x < 4; ++x) m.flags |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
+          for (int x = 0; x < KEYS / 16; ++x) m.flags |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
           m.pad[0] = m.pad[1] = 0;
           m.owner = blockIdx.x;
           m.n_parts = 1;
@@ -327,7 +331,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           if (I8) {
             float* sc = reinterpret_cast<float*>(side + s * SM::SIDE + NQ * D * 2) + lane * a.box_rows;
             bulk_load_1d(sc, a.k_scale + row, a.box_rows * 4, &full[s]);
-            bulk_load_1d(sc + DECODE_KEYS, a.v_scale + row, a.box_rows * 4, &full[s]);
+            bulk_load_1d(sc + KEYS, a.v_scale + row, a.box_rows * 4, &full[s]);
           }
         }
         ++it;
@@ -355,8 +359,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     auto head = [&](int x) { return I8 ? 4 * x + t : (x / 2) * 8 + 2 * t + (x & 1); };
     uint32_t qf[I8 ? HL : NT][KS][I8 ? 1 : 2];  // queries as the second operand
     float qs[HL];                               // int8: scale of the head's query
-    float acc[NT][KS][4];
+    float acc[I8 ? HL : NT][KS][I8 ? 2 : 4];    // element rows g, g + 8 (int8: 2g, 2g + 1) of each step
     float m[HL], l[HL];
+    auto out_at = [&](int x, int k, int r) -> float& { return acc[I8 ? x : x / 2][k][I8 ? r : (x & 1) + 2 * r]; };
     uint32_t met = 0, parity = 0;
     // bounded rendezvous of the four compute warps
     auto rendezvous = [&]() -> bool {
@@ -364,9 +369,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (lane == 0) mbar_arrive(meet);
       return mbar_wait_spin(meet, met++ & 1u, abort_flag, SITE_DECODE + 1);
     };
-    // this lane's ldmatrix rows inside a 16-key slice
-    const int box = 16 * warp / a.box_rows, row0 = 16 * warp - box * a.box_rows;
-    const uint32_t slice = box * a.box_rows * D * SM::ESZ + row0 * ROWB;
+    // where the 16 keys from `key` on begin inside a tile
+    auto slice_at = [&](int key) -> uint32_t {
+      const int box = key / a.box_rows;
+      return box * a.box_rows * D * SM::ESZ + (key - box * a.box_rows) * ROWB;
+    };
+    const uint32_t slice[2] = {slice_at(SLICE * warp), slice_at(SLICE * warp + (I8 ? 16 : 0))};
     const uint32_t half_step = a.box_rows * ROWB;
     auto line = [&](uint32_t base, int row, int c16) -> uint32_t {  // 16-byte piece c16 of a key's row
       const int h = c16 * 16 / ROWB, c = c16 % (ROWB / 16);
@@ -426,109 +434,148 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             }
         }
 #pragma unroll
-        for (int n = 0; n < NT; ++n)
+        for (int n = 0; n < (I8 ? HL : NT); ++n)
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[n][k][e] = 0.f;
+            for (int e = 0; e < (I8 ? 2 : 4); ++e) acc[n][k][e] = 0.f;
 #pragma unroll
         for (int x = 0; x < HL; ++x) m[x] = -INFINITY, l[x] = 0.f;
       }
-      const int left = block_left - 16 * warp;  // keys of this slice that exist
-      if (left > 0 && ((flags >> warp) & 1u)) {
-        const uint32_t kb = smem_addr(smem + s * SM::SLOT) + slice, vb = kb + SM::TILE;
-        float sc[HL][2];  // scores of keys g and g + 8, times log2(e)
-        float vs[2] = {1.f, 1.f};
-        if (I8) {
-          int c[HL][4] = {};
+      const int left = block_left - SLICE * warp;  // keys of this warp's share that exist
+      const unsigned there = (flags >> (SLICE / 16 * warp)) & (I8 ? 3u : 1u);
+      if (left > 0 && there) {
+        const uint32_t kb = smem_addr(smem + s * SM::SLOT), vb = kb + SM::TILE;
+        constexpr int NR = SLICE / 8;  // keys g + 8 r, r < NR, are this lane's
+        float sc[HL][NR];              // their scores, times log2(e)
+        float vs[NR];
+        if constexpr (I8) {
+          const float* scales = reinterpret_cast<const float*>(side + s * SM::SIDE + NQ * D * 2) + SLICE * warp + g;
 #pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            uint32_t r[4];
-            ldsm_x4(line(kb, lane & 15, k + (lane >> 4)), r);
+          for (int u = 0; u < 2; ++u) {
+            int c[HL][4] = {};
 #pragma unroll
-            for (int x = 0; x < HL; ++x) mma_16x8x32(c[I8 ? x : 0], r, qf[I8 ? x : 0][k][0], qf[I8 ? x : 0][k + 1][0]);
+            for (int k = 0; k < KS; k += 2) {
+              uint32_t r[4];
+              ldsm_x4(line(kb + slice[u], lane & 15, k + (lane >> 4)), r);
+#pragma unroll
+              for (int x = 0; x < HL; ++x) mma_16x8x32(c[x], r, qf[x][k][0], qf[x][k + 1][0]);
+            }
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+              const float ks = scales[16 * u + 8 * r] * a.scale_log2;
+              vs[2 * u + r] = scales[KEYS + 16 * u + 8 * r];
+#pragma unroll
+              for (int x = 0; x < HL; ++x)  // |256 hi + lo| < 2^30
+                sc[x][2 * u + r] = static_cast<float>(c[x][2 * r] * 256 + c[x][2 * r + 1]) * qs[x] * ks;
+            }
           }
-          const float* scales = reinterpret_cast<const float*>(side + s * SM::SIDE + NQ * D * 2) + 16 * warp + g;
-          const float ks[2] = {scales[0] * a.scale_log2, scales[8] * a.scale_log2};
-          vs[0] = scales[DECODE_KEYS];
-          vs[1] = scales[DECODE_KEYS + 8];
-#pragma unroll
-          for (int x = 0; x < HL; ++x)
-#pragma unroll
-            for (int r = 0; r < 2; ++r)  // |256 hi + lo| < 2^30
-              sc[x][r] = static_cast<float>(c[x][2 * r] * 256 + c[x][2 * r + 1]) * qs[x] * ks[r];
         } else {
           float c[NT][4] = {}, d[NT][4] = {};  // two chains of products
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t r[4];
-            ldsm_x4(line(kb, lane & 15, 2 * k + (lane >> 4)), r);
+            ldsm_x4(line(kb + slice[0], lane & 15, 2 * k + (lane >> 4)), r);
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-              mma_16x8x16(k & 1 ? d[n] : c[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][I8 ? 0 : 1]);
+            for (int n = 0; n < NT; ++n) mma_16x8x16(k & 1 ? d[n] : c[n], r[0], r[1], r[2], r[3], qf[n][k][0], qf[n][k][1]);
           }
 #pragma unroll
           for (int x = 0; x < HL; ++x)
 #pragma unroll
             for (int r = 0; r < 2; ++r) sc[x][r] = (c[x / 2][2 * r + (x & 1)] + d[x / 2][2 * r + (x & 1)]) * a.scale_log2;
         }
-        if (left < 16) {
+        if (left < SLICE || (I8 && there != 3u)) {
 #pragma unroll
-          for (int x = 0; x < HL; ++x)
+          for (int r = 0; r < NR; ++r)
+            if (g + 8 * r >= left || !((there >> (r / 2)) & 1u)) {
+              vs[r] = 0.f;
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-              if (g + 8 * r >= left) sc[x][r] = -INFINITY, vs[r] = 0.f;
+              for (int x = 0; x < HL; ++x) sc[x][r] = -INFINITY;
+            }
         }
         bool high = false;
 #pragma unroll
         for (int x = 0; x < HL; ++x)
 #pragma unroll
-          for (int r = 0; r < 2; ++r) high |= sc[x][r] > m[x] + 8.f;
+          for (int r = 0; r < NR; ++r) high |= sc[x][r] > m[x] + 8.f;
         if (__any_sync(0xFFFFFFFFu, high)) {
 #pragma unroll
           for (int x = 0; x < HL; ++x) {
-            float top = fmaxf(m[x], fmaxf(sc[x][0], sc[x][1]));
+            float top = m[x];
+#pragma unroll
+            for (int r = 0; r < NR; ++r) top = fmaxf(top, sc[x][r]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
             const float f = top > m[x] ? ex2_approx(m[x] - top) : 1.f;
             m[x] = top;
             l[x] *= f;
 #pragma unroll
-            for (int k = 0; k < KS; ++k) acc[x / 2][k][x & 1] *= f, acc[x / 2][k][(x & 1) + 2] *= f;
+            for (int k = 0; k < KS; ++k) out_at(x, k, 0) *= f, out_at(x, k, 1) *= f;
           }
         }
-        float p[2 * NT][2] = {};
+        float p[I8 ? HL : 2 * NT][NR] = {};
 #pragma unroll
         for (int x = 0; x < HL; ++x) {
           const float base = m[x] == -INFINITY ? 0.f : m[x];
 #pragma unroll
-          for (int r = 0; r < 2; ++r) {
+          for (int r = 0; r < NR; ++r) {
             p[x][r] = ex2_approx(sc[x][r] - base);
             l[x] += p[x][r];
             if (I8) p[x][r] *= vs[r];
           }
         }
-        uint32_t pb[NT][2];
+        if constexpr (I8) {
+          // probabilities times scales in 16-bit fixed point, of the largest
+          // among these 32 keys: hi and lo in the columns of the head
+          float ps[HL];
+          uint32_t pb[HL][2];
 #pragma unroll
-        for (int n = 0; n < NT; ++n)  // [key][head] to [head][key]: the second operand of the next product
+          for (int x = 0; x < HL; ++x) {
+            float top = max_nan(max_nan(p[x][0], p[x][1]), max_nan(p[x][2], p[x][3]));
 #pragma unroll
-          for (int r = 0; r < 2; ++r) pb[n][r] = transpose8x8(bf16x2_of(p[2 * n][r], p[2 * n + 1][r]));
-        if (I8) {
-          // a lane gets, for keys 2t and 2t + 1, elements 2g and 2g + 1: the
-          // even ones stand as rows g, the odd ones as rows g + 8
+            for (int o = 4; o < 32; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+            // (scaled up first where 1 / top would overflow)
+            const float up = top < 1e-30f ? 0x1p64f : 1.f, inv = top > 0.f ? __fdividef(32512.f, top * up) : 0.f;
+            ps[x] = top * (1.f / 32512.f);
+            uint32_t mv[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const int q = min(32512, __float2int_rn(p[x][r] * up * inv));
+              // hi = (q + 128) >> 8 in byte 0, lo in byte 2: [key][column] to [column][key]
+              mv[r] = transpose8x8(__byte_perm(q + 128, q, 0x4411));
+            }
+            pb[x][0] = __byte_perm(mv[0], mv[1], 0x6420);
+            pb[x][1] = __byte_perm(mv[2], mv[3], 0x6420);
+          }
+          // A lane gets, for keys 2t and 2t + 1 of each eight, elements 2g and
+          // 2g + 1: the even ones stand as rows g, the odd ones as rows g + 8,
+          // and the keys in the order of the probabilities' bytes.
 #pragma unroll
           for (int k = 0; k < KS; k += 2) {
-            uint32_t r[4];
-            ldsm_x4_t(line(vb, lane & 15, k + (lane >> 4)), r);
+            uint32_t r[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) ldsm_x4_t(line(vb + slice[u], lane & 15, k + (lane >> 4)), r[u]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const uint32_t a0 = codes_to_bf16(r[2 * h]), a1 = codes_to_bf16(r[2 * h] >> 8);
-              const uint32_t a2 = codes_to_bf16(r[2 * h + 1]), a3 = codes_to_bf16(r[2 * h + 1] >> 8);
+              const uint32_t a0 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x6420);
+              const uint32_t a1 = __byte_perm(r[0][2 * h], r[0][2 * h + 1], 0x7531);
+              const uint32_t a2 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x6420);
+              const uint32_t a3 = __byte_perm(r[1][2 * h], r[1][2 * h + 1], 0x7531);
 #pragma unroll
-              for (int n = 0; n < NT; ++n) mma_16x8x16(acc[n][k + h], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+              for (int x = 0; x < HL; ++x) {
+                int c[4];
+                mma_16x8x32_zero(c, a0, a1, a2, a3, pb[x][0], pb[x][1]);
+                acc[x][k + h][0] = fmaf(static_cast<float>(c[0] * 256 + c[1]), ps[x], acc[x][k + h][0]);
+                acc[x][k + h][1] = fmaf(static_cast<float>(c[2] * 256 + c[3]), ps[x], acc[x][k + h][1]);
+              }
             }
           }
         } else {
+          uint32_t pb[NT][2];
+#pragma unroll
+          for (int n = 0; n < NT; ++n)  // [key][head] to [head][key]: the second operand of the next product
+#pragma unroll
+            for (int r = 0; r < 2; ++r) pb[n][r] = transpose8x8(bf16x2_of(p[2 * n][r], p[2 * n + 1][r]));
           // rows past the end hold anything: 0 * NaN would be NaN
           uint32_t keep0 = 0xFFFFFFFFu, keep1 = 0xFFFFFFFFu;
           if (left < 16) {
@@ -538,7 +585,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
             uint32_t r[4];
-            ldsm_x4_t(line(vb, (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), r);
+            ldsm_x4_t(line(vb + slice[0], (lane & 7) + ((lane >> 4) << 3), 2 * k + ((lane >> 3) & 1)), r);
 #pragma unroll
             for (int n = 0; n < NT; ++n)
               mma_16x8x16(acc[n][k], r[0] & keep0, r[1] & keep0, r[2] & keep1, r[3] & keep1, pb[n][0], pb[n][1]);
@@ -580,8 +627,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           float* o = join + (warp * heads + h) * SM::PAD;
 #pragma unroll
           for (int k = 0; k < KS; ++k) {
-            o[16 * k + (I8 ? 2 * g : g)] = acc[x / 2][k][x & 1] * f;
-            o[16 * k + (I8 ? 2 * g + 1 : g + 8)] = acc[x / 2][k][(x & 1) + 2] * f;
+            o[16 * k + (I8 ? 2 * g : g)] = out_at(x, k, 0) * f;
+            o[16 * k + (I8 ? 2 * g + 1 : g + 8)] = out_at(x, k, 1) * f;
           }
         }
       }

@@ -76,7 +76,7 @@ def attention(q, k, v, scale, visible, v_scale=None):
             code = np.abs(v[see]) / np.where(v_scale[see] > 0, v_scale[see], 1)[:, None]
             for a in range(0, len(see), 32):
                 grid = grid + w[a:a + 32].max() / 65024 * code[a:a + 32].sum(0)
-        rel = BF16 + 2.0 ** -12 + 2 * ds + m * U
+        rel = (BF16 if v_scale is None else 0.0) + 2.0 ** -12 + 2 * ds + m * U
         tol[i] = (1 + BF16) * (rel * (p @ np.abs(v[see])) + grid) + BF16 * np.abs(o[i])
     return o, tol
 

@@ -108,7 +108,7 @@ def test_append_validation(lib):
 
 def _prompt(lib, **kw):
     a = dict(q=A, qs=512, k=A, ks=128, v=A, vs=128, tokens=4, kv=4, hq=4, hkv=1, d=128, cuq=A, cuk=A, seqs=2, scale=0.1,
-             causal=1, out=A, os=512)
+             causal=1, out=_p(0x20000), os=512)
     assert not set(kw) - set(a)
     return lib.convrot_attention_prompt(*(a | kw).values(), None)
 
@@ -121,6 +121,8 @@ def test_prompt_validation(lib):
     for name in ("q", "k", "v", "cuq", "cuk", "out"):
         assert _prompt(lib, **{name: None}) == 1, name
         assert _prompt(lib, **{name: _p(0x10002)}) == 3, name
+    for name in "qkv":                                            # in place is refused
+        assert _prompt(lib, **{name: _p(0x20000)}) == 4
     assert _prompt(lib, tokens=0, q=None) == 0 and _prompt(lib, seqs=0, q=None) == 0
 
 
@@ -140,6 +142,8 @@ def test_decode_validation(lib):
         assert _decode(lib, **{name: None}) == 1, name
         assert _decode(lib, **{name: _p(0x10002)}) == 3, name
     assert _decode(lib, sk=A) == 1
+    assert _decode(lib, ws=_p(0x10010), wb=1 << 30) == 3
+    assert _decode(lib, pages=1 << 21, page=4096, hkv=1, hq=1, qs=128, os=128) == 4  # rows of a TMA map: 31 bits
     assert _decode(lib, seqs=0, q=None) == 0
 
 

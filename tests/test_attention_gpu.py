@@ -226,6 +226,26 @@ def test_prompt(cr, lens, Hq, Hkv, D, causal):
     check_prompt(cr, *prompt_case(sum(lens) + Hq, lens, lens, Hq, Hkv, D), causal=causal)
 
 
+@pytest.mark.parametrize("n,Hq,Hkv,D", [(150, 4, 2, 64), (64, 2, 1, 128), (33, 8, 8, 128)])
+def test_prompt_many_sequences(cr, n, Hq, Hkv, D):
+    """More sequences than a warp has lanes, empty ones among them."""
+    lens = [(i * 29) % 41 if i % 3 else 0 for i in range(n)]
+    lens[-1] = 0
+    check_prompt(cr, *prompt_case(n, lens, lens, Hq, Hkv, D))
+
+
+def test_prompt_overlapping_offsets_end(cr):
+    """Offsets that go back and forth are no pack: reported, nothing hangs, and
+    nothing outside the rows is written."""
+    q, k, v, _, _ = prompt_case(12, [640], [640], 1, 1, 64)
+    big = torch.full((660, 1, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    for n in (3, 2001):
+        cu = torch.tensor([0, 640] * n, dtype=torch.int32, device="cuda")
+        cr.convrot_attention_prompt(q, k, v, cu, out=big[:640])
+        assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+        assert (big[640:] == 7).all()
+
+
 @pytest.mark.parametrize("causal", [True, False])
 @pytest.mark.parametrize("D", [64, 128])
 def test_prompt_with_keys_of_another_length(cr, D, causal):

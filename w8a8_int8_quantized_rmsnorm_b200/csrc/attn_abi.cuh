@@ -219,6 +219,7 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
       !stride_ok(v_stride, kv_heads, head_dim, kv_tokens) || !stride_ok(out_stride, q_heads, head_dim, tokens))
     return CONVROT_ERR_SHAPE;
   if (tokens == 0 || seqs == 0) return CONVROT_OK;
+  if (out == q || out == k || out == v) return CONVROT_ERR_UNSUPPORTED;  // q, k and v are read while out is written
   if (!q || !out || !cu_q || !cu_k || (kv_tokens > 0 && (!k || !v))) return CONVROT_ERR_NULL;
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
       !aligned(cu_k, 4))

@@ -669,7 +669,6 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       }
       if (!rendezvous()) break;
       if (threadIdx.x == 0) {
-        __threadfence();
         const unsigned before = atomic_add_acq_rel_gpu(&a.counters[b.owner], 1u);
         *is_last = before + 1 == static_cast<unsigned>(b.n_parts);
         if (before + 1 == static_cast<unsigned>(b.n_parts)) a.counters[b.owner] = 0;

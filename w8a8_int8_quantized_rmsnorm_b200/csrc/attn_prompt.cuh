@@ -369,12 +369,18 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       // one whose blocks come first, stays, and others follow as they come up.
       PromptChunk c;
       c.before = 0;
+      int64_t counted = 0;
       for (c.first = 0;; c.first += 32) {
         prompt_load(a, c);
+        const int n = __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+        counted += n;
         if (c.first + 32 >= a.seqs) break;
-        c.before += __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+        c.before += n;
       }
-      const int total = c.before + __shfl_sync(0xFFFFFFFFu, c.sum, 31);
+      // sequences that do not overlap have no more blocks than the grid has room for
+      const bool fits = counted * a.kv_heads * a.head_chunks <= gridDim.x;
+      if (!fits && lane == 0) report_error(ERR_BAD_ARGUMENT);
+      const int total = fits ? static_cast<int>(counted) : 0;
       const int heads = a.kv_heads * a.head_chunks;
       const int64_t units = static_cast<int64_t>(total) * heads;
       const int group = a.q_heads / a.kv_heads;

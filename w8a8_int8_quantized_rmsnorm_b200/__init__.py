@@ -467,13 +467,26 @@ def _cache(k_cache, v_cache, k_scale, v_scale):
     return shape
 
 
+def _current_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# the same handle without building a Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_stream)
+
+
 def _one_device(names, *operands):
     """_on_device for operands given in the order of `names`; returns the index
     of the device and its current stream's handle."""
     at = operands[0].get_device()
-    if at < 0 or at != torch.cuda.current_device() or any(t is not None and t.get_device() != at for t in operands):
-        _on_device(**dict(zip(names.split(), operands)))
-    return at, torch.cuda.current_stream(at).cuda_stream
+    if at >= 0 and at == torch.cuda.current_device():
+        for t in operands:
+            if t is not None and t.get_device() != at:
+                break
+        else:
+            return at, _raw_stream(at)
+    dev = _on_device(**dict(zip(names.split(), operands)))
+    return dev.index, _raw_stream(dev.index)
 
 
 def _at(t: Optional[torch.Tensor]):
@@ -505,7 +518,7 @@ def convrot_rope_append(q, k, v, rope, positions, slots, k_cache, v_cache, *, k_
     dev, stream = _one_device("q k v rope positions slots k_cache v_cache k_scale v_scale q_norm k_norm q_out k_out", q, k, v,
                               rope, positions, slots, k_cache, v_cache, k_scale, v_scale, q_norm, k_norm, q_out, k_out)
     if q_out is None:
-        q_out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
     R, turned = rope.shape
     _check("convrot_rope_append", lib().convrot_rope_append(
         q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, Hq, Hkv, D, rope.data_ptr(), R, turned, positions.data_ptr(),
@@ -536,7 +549,7 @@ def convrot_attention_prompt(q, k, v, cu_seqlens, cu_seqlens_k=None, *, scale: O
     so = _heads(out, "out", T, Hq, D)[3] if out is not None else Hq * D
     dev, stream = _one_device("q k v cu_seqlens cu_seqlens_k out", q, k, v, cu_seqlens, cu_seqlens_k, out)
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     _check("convrot_attention_prompt", lib().convrot_attention_prompt(
         q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T, Tk, Hq, Hkv, D, cu_seqlens.data_ptr(),
         cu_seqlens_k.data_ptr(), n, D ** -0.5 if scale is None else scale, int(causal), out.data_ptr(), so, stream))
@@ -545,6 +558,10 @@ def convrot_attention_prompt(q, k, v, cu_seqlens, cu_seqlens_k=None, *, scale: O
 
 def convrot_attention_decode_workspace_bytes(seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
     return int(lib().convrot_attention_decode_workspace_bytes(seqs, q_heads, kv_heads, head_dim))
+
+
+# workspace sizes by device and heads: they do not depend on the batch
+_decode_ws_bytes = {}
 
 
 def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_scale=None, v_scale=None,
@@ -569,12 +586,15 @@ def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_sc
     dev, stream = _one_device("q k_cache v_cache block_table seq_lens k_scale v_scale out", q, k_cache, v_cache, block_table,
                               seq_lens, k_scale, v_scale, out)
     if out is None:
-        out = torch.empty((B, Hq, D), dtype=torch.bfloat16, device=q.device)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
         # a captured graph gets its own: graphs may be replayed at the same time
         workspace = (Workspace(dev) if torch.cuda.is_current_stream_capturing() else
                      _default_ws.get((dev, stream)) or _default_ws.setdefault((dev, stream), Workspace(dev)))
-    ws, wn = workspace.get(convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D))
+    need = _decode_ws_bytes.get((dev, Hq, Hkv, D))
+    if need is None and B:
+        need = _decode_ws_bytes[dev, Hq, Hkv, D] = convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D)
+    ws, wn = workspace.get(need or 0)
     _check("convrot_attention_decode", lib().convrot_attention_decode(
         q.data_ptr(), sq, B, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), pages, page_size,
         block_table.data_ptr(), st if B > 1 else cols, cols, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,

@@ -19,13 +19,31 @@
 // last copies are under way it takes over the next unit that has not started
 // (clusterlaunchcontrol.try_cancel) instead of ending: a pack of very different
 // lengths spreads evenly, and set-up, fetch and store of neighbouring units
-// overlap.  Warps 0-3 and 4-7 each own one 128-row tile (a
-// thread owns a row; no exchange between threads), warp 8 fetches by TMA and
-// announces units, warp 9 issues the matrix products.  While one tile's
-// softmax runs, the tensor core works on the other's S or O.
+// overlap.  Warps 0-3 and 4-7 each own one 128-row tile (a thread owns a row; no
+// exchange between threads), warp 8 fetches by TMA and announces units, warp 9
+// issues the matrix products.  While one tile's softmax runs, the tensor core
+// works on the other's S or O.
 //
 // Tensor memory: S0, S1 (128 columns each; P overwrites its own S), O0, O1.
 // Shared memory: the two Q tiles and a ring of K and V tiles (128 keys).
+//
+// Measured (32 query heads on 8, D = 128, causal): 8192 tokens 491 us = 1.12
+// PFLOP/s (0.69 of cuBLAS's burst rate), 2048 tokens 40 us (256 units on 148
+// SMs), 34 prompts of 16 .. 300 tokens 43 us, 2.7 TB/s.  With D = 64, groups of 8
+// and 12 prompts of 1 .. 1333: 79 us.  What bounds a long prompt is a row tile's
+// turn: scores (512 cycles of tensor core), softmax (about 2200: 190 to fetch
+// the scores, 350 for the maximum, 1500 for 128 exponentials a row at 16 a cycle
+// and SM, 200 to hand P over), product with V (512).  Two row tiles take turns
+// in 3400 cycles where the tensor core alone needs 2048; tensor memory has no
+// room for a third.  Measured no faster: steps of 64 keys with two S buffers
+// (142 us for 4096 tokens instead of 116: 128 x 64 products are bound by the
+// reads of Q), P apart from S at D = 64 (104 instead of 99: without turns both
+// tiles reach their exponentials together), a quarter of the exponentials as a
+// cubic on the multiply-add pipe (the same at D = 128, 0.5 % less at D = 64),
+// three ring slots instead of four and room for whole result tiles (525 us for
+// 8192 tokens).  Handing units out by cluster launch control instead of a fixed
+// order took the ragged pack from 103 to 81 us.  A short prompt is bound by a
+// unit's chain of set-up, one softmax, product and store, 3.3 us.
 //
 // A probability of zero times an infinite or NaN value is NaN in the matrix
 // unit.  Such a value may sit in a masked place (a later token, the next
@@ -60,10 +78,6 @@ template <int D>
 struct PromptSmem {
   static constexpr int TILE = 128 * D * 2;                // bytes of a Q, K or V tile
   static constexpr int STAGES = D == 128 ? 4 : 8;
-  // One pair of exp2 in so many is a polynomial.  With D = 64 the exponential
-  // unit (16 a cycle) bounds: 4 x 1024 heads x tokens took 102 us without and 96
-  // us with; with D = 128 the tensor core does, and nothing was gained.
-  static constexpr int POLY = D == 128 ? 1 << 20 : 4;
   static constexpr int RING = 2 * TILE;
   static constexpr int OUT = RING + STAGES * TILE;        // a softmax warp's 32 result rows, 64 elements after 64
   static constexpr int BARS = OUT + 8 * 4096;
@@ -179,12 +193,6 @@ __device__ __forceinline__ bool elect_one() {
   return r != 0;
 }
 
-__device__ __forceinline__ float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float r;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -209,38 +217,9 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
   uint64_t r;
   asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-  return r;
-}
-
-// 2^x for two x <= 127 on the multiply-add pipe: x = i + f with i whole and
-// |f| <= 1/2 (adding 1.5 * 2^23 + 127 rounds x to a whole number and leaves
-// i + 127 in the low bits: the exponent of 2^i), times the cubic that fits 2^f
-// with the smallest relative error on that interval (7.5e-5; found by weighted
-// least squares with reweighting), a fiftieth of the rounding to bf16 that
-// follows.  x <= -127 gives exactly 0, a NaN stays one.
-__device__ __forceinline__ uint64_t exp2_poly2(float x0, float x1) {
-  constexpr float MAGIC = 12582912.f + 127.f;
-  const uint64_t x = pack2(max_nan(x0, -127.f), max_nan(x1, -127.f));
-  const uint64_t magic = pack2(MAGIC, MAGIC), t = add2(x, magic), f = sub2(x, sub2(t, magic));
-  uint64_t p = fma2(f, pack2(0.05517169f, 0.05517169f), pack2(0.24261117f, 0.24261117f));
-  p = fma2(f, p, pack2(0.69326097f, 0.69326097f));
-  p = fma2(f, p, pack2(0.99992806f, 0.99992806f));
-  float t0, t1;
-  unpack2(t, t0, t1);
-  return mul2(p, pack2(__uint_as_float(__float_as_uint(t0) << 23), __uint_as_float(__float_as_uint(t1) << 23)));
-}
-
-__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
-  uint32_t r;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
   return r;
 }
 
@@ -683,14 +662,10 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint32_t* in = &s[x][2 * e];
             float lo, hi;
             unpack2(fma2(pack2(__uint_as_float(in[0]), __uint_as_float(in[1])), c2, shift2), lo, hi);
-            if (e % SM::POLY == SM::POLY - 1) {
-              unpack2(exp2_poly2(lo, hi), lo, hi);
-            } else {
-              lo = ex2(lo);
-              hi = ex2(hi);
-            }
+            lo = ex2(lo);
+            hi = ex2(hi);
             sum2[e & 1] = add2(sum2[e & 1], pack2(lo, hi));
-            p[e] = cvt_bf16x2(lo, hi);
+            p[e] = bf16x2(lo, hi);
           }
           tmem_st_x16(t_s + 16 * x, p);
           if (x & 1) {  // half of the keys: the product with their values may begin
@@ -746,7 +721,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
             const uint64_t f = mul2(pack2(__uint_as_float(o[2 * e]), __uint_as_float(o[2 * e + 1])), inv2);
             nan2 = add2(nan2, f);
             unpack2(f, lo, hi);
-            r[e] = cvt_bf16x2(lo, hi);
+            r[e] = bf16x2(lo, hi);
           }
 #pragma unroll
           for (int e = 0; e < 4; ++e)

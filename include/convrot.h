@@ -427,8 +427,9 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  * out        bf16 [seqs, q_heads, D]  out
  * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte
  *            aligned, zero-filled before its first use; every call that
- *            completes leaves it zero, so the linears may share it.  Calls that
- *            overlap on the GPU need one each.
+ *            completes leaves it zero, so the linears may share it.  (This
+ *            entry itself needs only the first 4096 bytes to be zero.)  Calls
+ *            that overlap on the GPU need one each.
  */
 size_t convrot_attention_decode_workspace_bytes(int seqs, int q_heads, int kv_heads, int head_dim);
 convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seqs, int q_heads, int kv_heads,

@@ -570,6 +570,22 @@ def test_captured_append_and_prompt(cr):
     within(f64(o), ref_o, tol, "replayed prompt")
 
 
+def test_decode_refuses_a_short_workspace(cr):
+    import ctypes
+    c = decode_case(51, [70], 8, 2, 128, 16, False)
+    need = cr.convrot_attention_decode_workspace_bytes(1, 8, 2, 128)
+    ws = torch.zeros(need, dtype=torch.uint8, device="cuda")
+    out = torch.full((1, 8, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+    for p, n, want in ((None, need, 7), (ws.data_ptr(), need - 1, 7), (ws.data_ptr() + 16, need, 3), (ws.data_ptr(), need, 0)):
+        st = cr.lib().convrot_attention_decode(
+            c["q"].data_ptr(), 1024, 1, 8, 2, 128, c["k_cache"].data_ptr(), c["v_cache"].data_ptr(), None, None,
+            c["k_cache"].shape[0], 16, c["block_table"].data_ptr(), c["block_table"].shape[1], c["block_table"].shape[1],
+            c["seq_lens"].data_ptr(), 0.1, out.data_ptr(), 1024, p, n, ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+        torch.cuda.synchronize()
+        assert st == want
+        assert (out == 7).all() == (want != 0)
+
+
 def test_decode_leaves_its_workspace_zero(cr):
     """The linears' contract: a Workspace may serve both."""
     ws = cr.Workspace()

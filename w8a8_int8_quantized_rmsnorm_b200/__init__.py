@@ -588,13 +588,20 @@ def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_sc
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
     if workspace is None:
-        # a captured graph gets its own: graphs may be replayed at the same time
-        workspace = (Workspace(dev) if torch.cuda.is_current_stream_capturing() else
-                     _default_ws.get((dev, stream)) or _default_ws.setdefault((dev, stream), Workspace(dev)))
+        workspace = _default_ws.get((dev, stream)) or _default_ws.setdefault((dev, stream), Workspace(dev))
+        capturing = torch.cuda.is_current_stream_capturing()
+    else:
+        capturing = False
     need = _decode_ws_bytes.get((dev, Hq, Hkv, D))
     if need is None and B:
         need = _decode_ws_bytes[dev, Hq, Hkv, D] = convrot_attention_decode_workspace_bytes(B, Hq, Hkv, D)
-    ws, wn = workspace.get(need or 0)
+    if capturing and B:
+        # a captured graph gets its own: graphs may be replayed at the same time
+        own = torch.empty(need, dtype=torch.uint8, device=q.device)
+        own[:4096].zero_()
+        ws, wn = own.data_ptr(), need
+    else:
+        ws, wn = workspace.get(need or 0)
     _check("convrot_attention_decode", lib().convrot_attention_decode(
         q.data_ptr(), sq, B, Hq, Hkv, D, k_cache.data_ptr(), v_cache.data_ptr(), _at(k_scale), _at(v_scale), pages, page_size,
         block_table.data_ptr(), st if B > 1 else cols, cols, seq_lens.data_ptr(), D ** -0.5 if scale is None else scale,
@@ -764,7 +771,9 @@ class PagedKVCache:
         self.k_scale, self.v_scale = ((torch.zeros(shape[:3], device=dev) for _ in range(2)) if int8 else (None, None))
 
     def slots(self, block_table: torch.Tensor, sequence: torch.Tensor, position: torch.Tensor) -> torch.Tensor:
-        """Slots (int64) of tokens at `position` of rows `sequence` of the block table."""
+        """Slots (int64) of tokens at `position` of rows `sequence` of the block
+        table.  A page that is not there (negative) gives a negative slot: such
+        a token is not stored."""
         page = block_table[sequence.long(), position.long() // self.page_size].long()
         return page * self.page_size + position % self.page_size
 

@@ -92,12 +92,12 @@ int decode_unit_heads(int q_heads, int kv_heads) { return std::min(q_heads / kv_
 
 constexpr int kDecodeCtas = 2;  // most CTAs per SM of any decode kernel
 
-int decode_grid(const DeviceInfo& d) { return kDecodeCtas * d.sms; }
+int decode_grid(const DeviceInfo& d) { return std::min(kDecodeCtas * d.sms, 1024); }
 
-size_t decode_counter_bytes(int grid) { return (static_cast<size_t>(grid) * 4 + 255) / 256 * 256; }
+constexpr size_t kDecodeCounterBytes = 4096;  // a fixed region of counters at offset 0, one per CTA
 
 size_t decode_ws_bytes(int grid, int heads, int D) {
-  return decode_counter_bytes(grid) + static_cast<size_t>(grid) * 2 * decode_part_floats(heads, D) * sizeof(float);
+  return kDecodeCounterBytes + static_cast<size_t>(grid) * 2 * decode_part_floats(heads, D) * sizeof(float);
 }
 
 // A paged cache as a 3-D map (bytes or elements of a line, row, line of the
@@ -141,7 +141,7 @@ convrot_status run_decode(const DecodeArgs& args, const void* k_cache, const voi
       return CONVROT_ERR_CUDA;
     configured[d.device].store(true, std::memory_order_release);
   }
-  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(SM::CTAS * d.sms, blocks));
+  const unsigned grid = static_cast<unsigned>(std::min<int64_t>(std::min(SM::CTAS * d.sms, 1024), blocks));
   return launch_pdl(k, dim3(grid), dim3(DECODE_THREADS), smem, st, 1, mk, mv, a);
 }
 
@@ -300,7 +300,7 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   const int grid = decode_grid(d);
   if (!workspace || workspace_bytes < decode_ws_bytes(grid, a.chunk_heads, head_dim)) return CONVROT_ERR_WORKSPACE;
   a.counters = static_cast<unsigned*>(workspace);
-  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + decode_counter_bytes(grid));
+  a.parts = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + kDecodeCounterBytes);
   // no more CTAs than blocks there can be
   const int keys = k_scale ? DecodeSmem<128, true, 8>::KEYS : DecodeSmem<128, false, 8>::KEYS;
   const int64_t most = std::max<int64_t>(1, (static_cast<int64_t>(table_cols) * page_size + keys - 1) / keys);

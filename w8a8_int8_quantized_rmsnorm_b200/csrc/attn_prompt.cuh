@@ -28,22 +28,26 @@
 // Shared memory: the two Q tiles and a ring of K and V tiles (128 keys).
 //
 // Measured (32 query heads on 8, D = 128, causal): 8192 tokens 491 us = 1.12
-// PFLOP/s (0.69 of cuBLAS's burst rate), 2048 tokens 40 us (256 units on 148
+// PFLOP/s (0.69 of cuBLAS's burst rate), 2048 tokens 41 us (256 units on 148
 // SMs), 34 prompts of 16 .. 300 tokens 43 us, 2.7 TB/s.  With D = 64, groups of 8
-// and 12 prompts of 1 .. 1333: 79 us.  What bounds a long prompt is a row tile's
-// turn: scores (512 cycles of tensor core), softmax (about 2200: 190 to fetch
-// the scores, 350 for the maximum, 1500 for 128 exponentials a row at 16 a cycle
-// and SM, 200 to hand P over), product with V (512).  Two row tiles take turns
-// in 3400 cycles where the tensor core alone needs 2048; tensor memory has no
-// room for a third.  Measured no faster: steps of 64 keys with two S buffers
-// (142 us for 4096 tokens instead of 116: 128 x 64 products are bound by the
-// reads of Q), P apart from S at D = 64 (104 instead of 99: without turns both
-// tiles reach their exponentials together), a quarter of the exponentials as a
-// cubic on the multiply-add pipe (the same at D = 128, 0.5 % less at D = 64),
-// three ring slots instead of four and room for whole result tiles (525 us for
-// 8192 tokens).  Handing units out by cluster launch control instead of a fixed
-// order took the ragged pack from 103 to 81 us.  A short prompt is bound by a
-// unit's chain of set-up, one softmax, product and store, 3.3 us.
+// and 12 prompts of 1 .. 1333: 77 us.
+//
+// What bounds a long prompt is the round of one row tile, 3300 cycles: scores
+// (590: both operands come from shared memory, 8 KB per 64 cycles, its whole
+// bandwidth), fetching them 190, maximum 430, 128 exponentials a row 1500, the
+// rest of the product with V 256, and four hand-overs between the issuing warp
+// and the softmax.  The two row tiles take turns; the tensor core needs 2200 of
+// those cycles.  No single part is the limit: without exponentials, maxima and
+// conversions 4096 tokens still took 110 us of 115.  Tensor memory has no room
+// for a third row tile.  Measured no faster: steps of 64 keys with two S buffers
+// (142 us for 4096 tokens: 128 x 64 products are bound by the reads of Q), P
+// apart from S at D = 64 (104 us instead of 99: without turns both tiles reach
+// their exponentials together), a quarter of the exponentials as a cubic on the
+// multiply-add pipe (the same at D = 128, 0.5 % less at D = 64), three ring slots
+// instead of four and room for whole result tiles (525 us for 8192 tokens).
+// Handing units out by cluster launch control instead of a fixed order took the
+// ragged pack from 103 to 81 us.  A short prompt is bound by a unit's chain of
+// set-up, one softmax, product and store, 3.3 us.
 //
 // A probability of zero times an infinite or NaN value is NaN in the matrix
 // unit.  Such a value may sit in a masked place (a later token, the next
@@ -113,25 +117,38 @@ __device__ __forceinline__ uint32_t mnmajor_desc(uint32_t saddr, uint32_t next64
   return ((saddr & 0x3FFFFu) >> 4) | ((next64 >> 4) << 16);
 }
 
-// D[tmem] (+)= A[smem] * B[smem]^T, 128 x N x 16 bf16.
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// Products are issued by a warp's elected lane, four to a statement.
+//
+// D[tmem] (+)= A[smem] * B[smem]^T over 64 elements (128 bytes) of a K-major
+// line: 128 x N x 64 bf16.
+__device__ __forceinline__ void mma_ss_x4(uint32_t d_tmem, uint32_t adesc, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 a, b, a1, b1, a2, b2, a3, b3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "mov.b64 a, {%1, %5};\n\tmov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+      "add.s64 a1, a, 2;\n\tadd.s64 b1, b, 2;\n\t"
+      "add.s64 a2, a, 4;\n\tadd.s64 b2, b, 4;\n\t"
+      "add.s64 a3, a, 6;\n\tadd.s64 b3, b, 6;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %3, t;\n\t}" ::"r"(d_tmem),
       "r"(adesc), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
       : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem]^T, 128 x N x 16 bf16.
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D[tmem] (+)= A[tmem] * B[smem]^T over 64 keys (lines of 128 bytes, 16 to a
+// product): 128 x N x 64 bf16.
+__device__ __forceinline__ void mma_ts_x4(uint32_t d_tmem, uint32_t a_tmem, uint32_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
+      "{\n\t.reg .pred p, t;\n\t.reg .b64 b, b1, b2, b3;\n\t.reg .b32 a1, a2, a3;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\tsetp.eq.b32 t, 0, 0;\n\t"
       "mov.b64 b, {%2, %5};\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+      "add.s64 b1, b, 128;\n\tadd.s64 b2, b, 256;\n\tadd.s64 b3, b, 384;\n\t"
+      "add.u32 a1, %1, 8;\n\tadd.u32 a2, %1, 16;\n\tadd.u32 a3, %1, 24;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], b1, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], b2, %3, t;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b3, %3, t;\n\t}" ::"r"(d_tmem),
       "r"(a_tmem), "r"(bdesc), "r"(idesc), "r"(accumulate), "r"(DESC_HIGH)
       : "memory");
 }
@@ -477,34 +494,22 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const uint32_t qd = __shfl_sync(0xFFFFFFFFu, kmajor_desc(smem_addr(smem)), 0);
       const uint32_t kd = __shfl_sync(0xFFFFFFFFu, kmajor_desc(smem_addr(smem + SM::RING)), 0);
       const uint32_t vd = __shfl_sync(0xFFFFFFFFu, mnmajor_desc(smem_addr(smem + SM::RING), 16384), 0);
+      // (all three inside an elected lane's branch)
       auto scores = [&](int w, uint32_t stage, bool last) {
-        if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < D / 16; ++k) {
-            // 32 bytes along a 128-byte line; the second half of the row is 16 KB on
-            const uint32_t off = (k / 4) * (16384 >> 4) + (k % 4) * 2;
-            mma_ss(tm + TM_S + w * 128, qd + w * (SM::TILE >> 4) + off, kd + stage * (SM::TILE >> 4) + off, idesc_s, k > 0);
-          }
-          mma_commit(&s_full[w]);
-          if (last) mma_commit(&q_empty[w]);
-        }
+        for (int h = 0; h < HALVES; ++h)  // the second half of the rows is 16 KB on
+          mma_ss_x4(tm + TM_S + w * 128, qd + w * (SM::TILE >> 4) + h * (16384 >> 4),
+                    kd + stage * (SM::TILE >> 4) + h * (16384 >> 4), idesc_s, h > 0);
+        mma_commit(&s_full[w]);
+        if (last) mma_commit(&q_empty[w]);
       };
       auto values = [&](int w, uint32_t stage, int half, bool accumulate) {  // 64 keys
-        if (elect_one()) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {  // 16 keys: 16 lines of 128 bytes
-            const int k = 4 * half + x;
-            mma_ts(tm + TM_O + w * 128, tm + TM_S + w * 128 + k * 8, vd + stage * (SM::TILE >> 4) + k * (2048 >> 4), idesc_o,
-                   accumulate || x > 0);
-          }
-          if (half) mma_commit(&o_done[w]);
-        }
+        mma_ts_x4(tm + TM_O + w * 128, tm + TM_S + w * 128 + half * 32, vd + stage * (SM::TILE >> 4) + half * (8192 >> 4),
+                  idesc_o, accumulate);
       };
-      auto release = [&](uint32_t stage) {
-        if (elect_one()) mma_commit(&kv_empty[stage]);
-      };
+      auto release = [&](uint32_t stage) { mma_commit(&kv_empty[stage]); };
       // A wait that gives up has raised the abort flag, which the warp looks at
-      // together, once per tile: until then it issues on without harm, since a
+      // together, once in eight tiles: until then it issues on without harm, since a
       // product touches this CTA's own memory only.
       auto wait = [&](uint64_t* bar, uint32_t parity, unsigned site) { prompt_wait(bar, parity, abort_flag, busy, site); };
       auto going = [&]() -> bool { return __all_sync(0xFFFFFFFFu, *abort_flag == 0); };
@@ -529,39 +534,59 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           wait(&q_full[w], q_use[w] & 1u, SITE_ATTN + 2);
           ++q_use[w];
           tc_fence_after();
-          scores(w, stage, nw[w] == 1);
+          if (elect_one()) scores(w, stage, nw[w] == 1);
         }
-        release(stage);
+        if (elect_one()) release(stage);
         advance(stage, phase);
         int j = 0;
-        for (; j < n && going(); ++j) {
+        bool here = false;  // this tile's copies have been seen to be in
+        for (; j < n && ((j & 7) || going()); ++j) {
           uint32_t sk = stage, phase_k = phase;  // values at `stage`, the next keys behind them
           advance(sk, phase_k);
-          wait(&kv_full[stage], phase, SITE_ATTN + 2);
-          if (j + 1 < n) wait(&kv_full[sk], phase_k, SITE_ATTN + 2);
+          if (!here) {
+            wait(&kv_full[stage], phase, SITE_ATTN + 2);
+            if (j + 1 < n) wait(&kv_full[sk], phase_k, SITE_ATTN + 2);
+          }
+          here = false;
+          uint32_t sv = j + 1 < n ? sk : stage, phase_v = j + 1 < n ? phase_k : phase;  // the next tile's values
+          advance(sv, phase_v);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            if (j >= nw[w]) continue;
-            wait(&p_full[w], p_use[w] & 1u, SITE_ATTN + 3);
-            ++p_use[w];
-            tc_fence_after();
-            values(w, stage, 0, j > 0);
-            if (2 * j + 2 > nh[w]) {  // a last tile's first half is all there is
-              if (elect_one()) mma_commit(&o_done[w]);
-              continue;
+            if (j < nw[w]) {
+              wait(&p_full[w], p_use[w] & 1u, SITE_ATTN + 3);
+              ++p_use[w];
+              tc_fence_after();
+              if (elect_one()) values(w, stage, 0, j > 0);
+              if (2 * j + 2 > nh[w]) {  // a last tile's first half is all there is
+                if (elect_one()) mma_commit(&o_done[w]);
+              } else {
+                wait(&p_rest[w], rest_use[w] & 1u, SITE_ATTN + 3);
+                ++rest_use[w];
+                tc_fence_after();
+                if (elect_one()) {
+                  values(w, stage, 1, true);
+                  if (j + 1 < nw[w])
+                    scores(w, sk, j + 2 == nw[w]);
+                  else
+                    mma_commit(&o_done[w]);
+                }
+              }
             }
-            wait(&p_rest[w], rest_use[w] & 1u, SITE_ATTN + 3);
-            ++rest_use[w];
-            tc_fence_after();
-            values(w, stage, 1, true);
-            if (j + 1 < nw[w]) scores(w, sk, j + 2 == nw[w]);
+            // a look at the next tile's copies while the other row tile is at work
+            if (w == 0 && j + 1 < n) {
+              here = mbar_try_wait(&kv_full[sv], phase_v);
+              if (j + 2 < n) {
+                uint32_t s2 = sv, phase_2 = phase_v;
+                advance(s2, phase_2);
+                here = mbar_try_wait(&kv_full[s2], phase_2) && here;
+              }
+            }
           }
-          release(stage);
-          if (j + 1 < n) {
-            release(sk);
-            stage = sk, phase = phase_k;
+          if (elect_one()) {
+            release(stage);
+            if (j + 1 < n) release(sk);
           }
-          advance(stage, phase);
+          stage = sv, phase = phase_v;
         }
         if (j < n) break;
       }
@@ -581,7 +606,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
     const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const uint32_t t_s = tmem + lanes + TM_S + w * 128, t_o = tmem + lanes + TM_O + w * 128;
     const float c = a.scale_log2, raise = 8.f / c;
-    uint32_t s_use = 0;  // S tiles taken so far = O products awaited or not
+    uint32_t s_use = 0, o_use = 0;  // score tiles and results taken so far
     for (uint32_t n_info = 0;; ++n_info) {
       if (!prompt_wait(&info_full[n_info & 1u], (n_info >> 1) & 1u, abort_flag, busy, SITE_ATTN + 4)) break;
       const PromptUnit& u = info[n_info & 1u];  // read where it is needed: registers are short
@@ -637,9 +662,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
           const float f = m_new == m ? 1.f : ex2((m - m_new) * c);
           m = m_new;
           l *= f;
-          ok = prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5);
-          if (!ok) break;
-          tc_fence_after();
+          // (the product before these scores is complete: they were issued after it)
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {  // (sixteen at a time: the scores stay in registers)
             uint32_t o[16];
@@ -691,7 +714,7 @@ prompt_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ 
       const bool boxed = a.boxed && stored == 0xFFFFFFFFu;
       uint64_t nan2 = 0;
       if (n_tiles > 0) {
-        if (!prompt_wait(&o_done[w], (s_use - 1) & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
+        if (!prompt_wait(&o_done[w], o_use++ & 1u, abort_flag, busy, SITE_ATTN + 5)) break;
         tc_fence_after();
       }
       const float inv = lim > 0 ? 1.f / l : 0.f;

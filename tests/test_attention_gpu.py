@@ -681,3 +681,65 @@ def test_decode_step_agrees_with_the_prompt_s_last_row(cr):
     o, tol = ref.packed_attention(f64(q[-1:]), f64(k), f64(c["v"]), [0, 1], [0, n], D ** -0.5, True)
     within(f64(a), o[0], tol[0], "prompt")
     within(f64(b), o[0], tol[0], "decode")
+
+
+# ------------------------------------------------------------------ the ends of the ranges
+def test_empty_calls(cr):
+    """No tokens, no sequences, no keys at all."""
+    q, k = randn(1, 5, 4, 64), torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu, none = torch.tensor([0, 3, 5], dtype=torch.int32).cuda(), torch.zeros(3, dtype=torch.int32).cuda()
+    assert not cr.convrot_attention_prompt(q, k, k, cu, none).any()
+    assert not cr.convrot_attention_prompt(q, k, k, cu, none, causal=False).any()
+    out = torch.full_like(q, 7.0)
+    cr.convrot_attention_prompt(q, q, q, torch.zeros(1, dtype=torch.int32).cuda(), out=out)   # no sequence
+    assert (out == 7).all()
+    assert cr.convrot_attention_prompt(q[:0], k, k, none).shape == (0, 4, 64)
+    c = append_case(1, 4, 4, 2, 64, 64, 16, False, False)
+    c = {n: t[:0] if n in ("q", "k", "v", "positions", "slots") else t for n, t in c.items()}
+    before = c["k_cache"].clone()
+    assert cr.convrot_rope_append(**c)[0].shape == (0, 4, 64) and torch.equal(before, c["k_cache"])
+    d = decode_case(2, [5], 4, 2, 64, 16, False)
+    assert cr.convrot_attention_decode(d["q"][:0], d["k_cache"], d["v_cache"], d["block_table"][:0],
+                                       d["seq_lens"][:0]).shape == (0, 4, 64)
+    assert cr.convrot_device_status() == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_one_key_head_for_very_many(cr, D):
+    check_prompt(cr, *prompt_case(3, [19, 2], [19, 2], 1024, 1, D))
+    check_decode(cr, decode_case(4, [33, 200], 1024, 1, D, 32, True), [33, 200])
+    c = append_case(5, 9, 1000, 25, D, D, 16, True, True)
+    before, q, k = run_append(cr, c)
+    check_append(c, before, q, k)
+
+
+def test_prompts_on_two_streams_at_once(cr):
+    cases = []
+    for i, lens in enumerate(([700, 3, 130], [1025, 64])):
+        q, k, v, cu, _ = prompt_case(70 + i, lens, lens, 8, 2, 128 if i else 64)
+        cases.append((q, k, v, torch.from_numpy(cu).cuda()))
+    want = [cr.convrot_attention_prompt(*c) for c in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(20):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(cr.convrot_attention_prompt(*cases[i]))
+    torch.cuda.synchronize()
+    for g, w in zip(got, want):
+        assert all(torch.equal(x, w) for x in g)
+    assert cr.convrot_device_status() == 0
+
+
+def test_long_prompt_rows(cr):
+    """Rows spread over a long prompt: many tiles, references raised on the way."""
+    n, Hq, Hkv, D = 5003, 4, 1, 128
+    q, k, v, cu, _ = prompt_case(80, [n], [n], Hq, Hkv, D)
+    k[n // 2:] = k[n // 2:].float() * 3          # later keys score far higher
+    got = f64(cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda()))
+    K, V = f64(k)[:, 0], f64(v)[:, 0]
+    for t in (0, 1, 63, 64, 127, 128, 1000, n // 2 - 1, n // 2, n // 2 + 1, 4095, 4096, n - 2, n - 1):
+        for h in range(Hq):
+            o, tol = ref.attention(f64(q[t])[h][None], K, V, D ** -0.5, np.arange(n)[None] <= t)
+            within(got[t, h], o[0], tol[0], f"row {t} head {h}")

@@ -292,6 +292,20 @@ def test_prompt_masked_places_do_not_leak(cr, bad, D, Hq, Hkv):
         assert np.isnan(got[180:201]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prompt_nan_in_one_element_of_a_seen_value(cr, D):
+    """It reaches that element of the rows that see it, and nothing else."""
+    q, k, v, cu, _ = prompt_case(5, [230], [230], 4, 2, D)
+    clean = v.clone()
+    v[100, 1, 5] = float("nan")
+    got = f64(cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda()))
+    o, tol = ref.packed_attention(f64(q), f64(k), f64(clean), cu, cu, D ** -0.5, True)
+    hit = np.zeros(got.shape, bool)
+    hit[100:, 2:, 5] = True
+    assert np.isnan(got[hit]).all()
+    within(got[~hit], o[~hit], tol[~hit], "the others")
+
+
 def test_prompt_scores_of_minus_infinity_and_large_scores(cr):
     q, k, v, cu, _ = prompt_case(6, [160], [160], 2, 1, 128)
     q[:, :, 0], k[:, :, 0] = 300.0, 0.0

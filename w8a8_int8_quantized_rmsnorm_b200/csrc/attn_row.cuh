@@ -34,29 +34,33 @@ __device__ __forceinline__ uint32_t bf16x2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ float bf16_at(const uint16_t* p, int i) {
-  return __uint_as_float(static_cast<uint32_t>(p[i]) << 16);
-}
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xFFFF0000u); }
 
 // q: D bf16 of the row; k, v: the first key's and value's row of the head, the
 // next ones k_stride and v_stride elements on; o: D bf16.  The whole warp calls.
+// A lane reads its key's row 16 bytes at a time (the query's too, all lanes the
+// same piece) and holds D / 32 neighbouring elements of the result.  A row that
+// is NaN throughout ends at the key that made it so.
 template <int D>
 __device__ void attention_row(const uint16_t* q, const uint16_t* k, int64_t k_stride, const uint16_t* v,
                               int64_t v_stride, int n, float scale_log2, uint16_t* o) {
   constexpr int E = D / 32;
   const int lane = threadIdx.x & 31;
-  float qe[E], acc[E] = {};
-#pragma unroll
-  for (int e = 0; e < E; ++e) qe[e] = bf16_at(q, e * 32 + lane);
+  float acc[E] = {};
   float m = -INFINITY, l = 0.f;
   for (int j0 = 0; j0 < n; j0 += 32) {
     const int j = j0 + lane;
-    const uint16_t* kj = k + static_cast<int64_t>(min(j, n - 1)) * k_stride;
+    const uint4* kj = reinterpret_cast<const uint4*>(k + static_cast<int64_t>(min(j, n - 1)) * k_stride);
     float s = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e)
-      for (int i = 0; i < 32; ++i)
-        s = fmaf(__shfl_sync(0xFFFFFFFFu, qe[e], i), bf16_at(kj, e * 32 + i), s);
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const uint4 x = kj[c], y = reinterpret_cast<const uint4*>(q)[c];
+      s = fmaf(bf16_lo(x.x), bf16_lo(y.x), fmaf(bf16_hi(x.x), bf16_hi(y.x), s));
+      s = fmaf(bf16_lo(x.y), bf16_lo(y.y), fmaf(bf16_hi(x.y), bf16_hi(y.y), s));
+      s = fmaf(bf16_lo(x.z), bf16_lo(y.z), fmaf(bf16_hi(x.z), bf16_hi(y.z), s));
+      s = fmaf(bf16_lo(x.w), bf16_lo(y.w), fmaf(bf16_hi(x.w), bf16_hi(y.w), s));
+    }
     s = j < n ? s * scale_log2 : -INFINITY;
     float top = s;
 #pragma unroll
@@ -70,20 +74,31 @@ __device__ void attention_row(const uint16_t* q, const uint16_t* k, int64_t k_st
     l = l * old + p;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] *= old;
-    for (int i = 0; i < min(32, n - j0); ++i) {
+#pragma unroll 4
+    for (int i = 0; i < 32; ++i) {
       const float pi = __shfl_sync(0xFFFFFFFFu, p, i);
-      const uint16_t* vi = v + static_cast<int64_t>(j0 + i) * v_stride;
+      if (j0 + i >= n) break;  // the same for the whole warp
+      const uint32_t* vi = reinterpret_cast<const uint32_t*>(v + static_cast<int64_t>(j0 + i) * v_stride + lane * E);
 #pragma unroll
-      for (int e = 0; e < E; ++e) acc[e] = fmaf(pi, bf16_at(vi, e * 32 + lane), acc[e]);
+      for (int e = 0; e < E; e += 2) {
+        const uint32_t w = vi[e / 2];
+        acc[e] = fmaf(pi, bf16_lo(w), acc[e]);
+        acc[e + 1] = fmaf(pi, bf16_hi(w), acc[e + 1]);
+      }
+    }
+    bool lost = true;
+#pragma unroll
+    for (int e = 0; e < E; ++e) lost &= acc[e] != acc[e];
+    if (__any_sync(0xFFFFFFFFu, p != p) || __all_sync(0xFFFFFFFFu, lost)) {
+      l = NAN;
+      break;
     }
   }
 #pragma unroll
   for (int x = 16; x; x >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, x);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const __nv_bfloat16 r = __float2bfloat16(n > 0 ? acc[e] / l : 0.f);
-    o[e * 32 + lane] = __bfloat16_as_ushort(r);
-  }
+  for (int e = 0; e < E; e += 2)
+    reinterpret_cast<uint32_t*>(o + lane * E)[e / 2] = n > 0 ? bf16x2(acc[e] / l, acc[e + 1] / l) : 0u;
 }
 
 }  // namespace convrot

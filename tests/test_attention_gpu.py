@@ -757,3 +757,60 @@ def test_long_prompt_rows(cr):
         for h in range(Hq):
             o, tol = ref.attention(f64(q[t])[h][None], K, V, D ** -0.5, np.arange(n)[None] <= t)
             within(got[t, h], o[0], tol[0], f"row {t} head {h}")
+
+# ------------------------------------------------------------------ many blocks per CTA
+def long_decode_case(seed, lens, Hq, Hkv, D, page, i8):
+    """Contexts of thousands of keys, made on the GPU; keys of the later half of
+    every page row score three times as high as the others."""
+    g = torch.Generator("cuda").manual_seed(seed)
+    need = [-(-n // page) for n in lens]
+    pages = sum(need) + 2
+    perm = torch.randperm(pages, generator=g, device="cuda").int()
+    table = torch.full((len(lens), max(need)), -7, dtype=torch.int32, device="cuda")
+    at = 0
+    for i, n in enumerate(need):
+        table[i, :n] = perm[at:at + n]
+        at += n
+    shape = (pages, Hkv, page, D)
+    c = dict(q=(torch.randn(len(lens), Hq, D, generator=g, device="cuda") * 2).to(torch.bfloat16), block_table=table,
+             seq_lens=torch.tensor(lens, dtype=torch.int32).cuda())
+    wide = torch.zeros(pages, dtype=torch.bool, device="cuda")
+    for i, n in enumerate(need):
+        wide[table[i, n // 2:n].long()] = True
+    for x in "kv":
+        if i8:
+            c[x + "_cache"] = torch.randint(-127, 128, shape, generator=g, device="cuda", dtype=torch.int16).to(torch.int8)
+            c[x + "_scale"] = torch.rand(shape[:3], generator=g, device="cuda") * 0.02 + 0.005
+        else:
+            c[x + "_cache"] = torch.randn(shape, generator=g, device="cuda").to(torch.bfloat16)
+    c["k_scale" if i8 else "k_cache"][wide] *= 3
+    return c
+
+
+LONG = [(32, 8, 128, 16), (64, 8, 128, 48), (16, 4, 64, 64), (16, 2, 64, 128), (20, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page", LONG)
+def test_decode_heads_do_not_touch_one_another(cr, Hq, Hkv, D, page, i8):
+    """A head's result depends, bit by bit, on its own query alone: other
+    queries of its group, and what other kernels left in shared memory, move
+    nothing."""
+    lens = [3000 - 17 * i for i in range(160 // Hkv)]
+    c = long_decode_case(7, lens, Hq, Hkv, D, page, i8)
+    want = cr.convrot_attention_decode(**c)
+    group = Hq // Hkv
+    first = torch.arange(Hq, device="cuda") % group == 0
+    other = dict(c, q=torch.where(first[:, None], c["q"], (c["q"].float() * 8).to(torch.bfloat16)))
+    got = cr.convrot_attention_decode(**other)
+    assert torch.equal(got[:, first], want[:, first])
+    noise = long_decode_case(8, lens, 16, 1, 128, 16, not i8)
+    noise["q"] *= 30
+    p = prompt_case(9, [700], [700], 8, 2, 128)
+    for i in range(6):
+        if i % 2:
+            cr.convrot_attention_decode(**noise)
+        else:
+            cr.convrot_attention_prompt(*(x * 100 for x in p[:3]), torch.from_numpy(p[3]).cuda())
+        assert torch.equal(cr.convrot_attention_decode(**c), want)
+    assert cr.convrot_device_status() == 0

@@ -81,7 +81,8 @@ struct DecodeBlock {
   unsigned flags;       // bits 0-7: the 16-key slices that are there; then:
   int seq, unit;        // unit: (kv head, head chunk)
   int owner, n_parts;   // CTA of the (seq, unit)'s first block; parts (1: whole)
-  int pad[2];
+  int heads;            // query heads of the unit that there are
+  int pad;
 };
 // begins / ends this CTA's stretch of the (seq, unit); no more blocks
 constexpr unsigned BLOCK_FIRST = 256, BLOCK_LAST = 512, BLOCK_END = 1024;
@@ -304,7 +305,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
           m.left = cur.len - j * KEYS;
           m.flags = (first ? BLOCK_FIRST : 0) | (last ? BLOCK_LAST : 0);
           for (int x = 0; x < KEYS / 16; ++x) m.flags |= ((mask >> (16 * x / a.box_rows)) & 1u) << x;
-          m.pad[0] = m.pad[1] = 0;
+          m.heads = qh;
+          m.pad = 0;
           m.owner = blockIdx.x;
           m.n_parts = 1;
           if (last && (item < begin || item + cur.nb > end)) {  // twice per CTA at most: its two ends
@@ -388,6 +390,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       if (flags & BLOCK_END) break;
       if (flags & BLOCK_FIRST) {
         const uint8_t* rows = side + s * SM::SIDE;
+        const int live = meta[s].heads;  // the rows past them hold anything: zero
         if (I8) {
           // columns 2h and 2h + 1 of a tile: hi and lo of head h; this lane's is column g
 #pragma unroll
@@ -396,7 +399,8 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             float v[KS][4], top = 0.f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
-              const uint2 w = *reinterpret_cast<const uint2*>(p + 32 * k);  // elements 16k + 4t ..
+              uint2 w = make_uint2(0, 0);
+              if (4 * x + (g >> 1) < live) w = *reinterpret_cast<const uint2*>(p + 32 * k);  // elements 16k + 4t ..
               v[k][0] = __uint_as_float(w.x << 16), v[k][1] = __uint_as_float(w.x & 0xFFFF0000u);
               v[k][2] = __uint_as_float(w.y << 16), v[k][3] = __uint_as_float(w.y & 0xFFFF0000u);
 #pragma unroll
@@ -426,8 +430,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
               const uint8_t* p = rows + ((n * 8 + g) * D + k * 16) * 2;
-              qf[n][k][0] = *reinterpret_cast<const uint32_t*>(p + 4 * t);
-              qf[n][k][I8 ? 0 : 1] = *reinterpret_cast<const uint32_t*>(p + 16 + 4 * t);
+              const bool mine = n * 8 + g < live;
+              qf[n][k][0] = mine ? *reinterpret_cast<const uint32_t*>(p + 4 * t) : 0u;
+              qf[n][k][I8 ? 0 : 1] = mine ? *reinterpret_cast<const uint32_t*>(p + 16 + 4 * t) : 0u;
             }
         }
 #pragma unroll
@@ -503,8 +508,10 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int r = 0; r < NR; ++r) top = fmaxf(top, sc[x][r]);
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            const float f = top > m[x] ? ex2(m[x] - top) : 1.f;
-            m[x] = top;
+            // each head by its own scores: its result depends on nothing else
+            const bool up = top > m[x] + 8.f;
+            const float f = up ? ex2(m[x] - top) : 1.f;
+            if (up) m[x] = top;
             l[x] *= f;
 #pragma unroll
             for (int k = 0; k < KS; ++k) out_at(x, k, 0) *= f, out_at(x, k, 1) *= f;

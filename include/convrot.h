@@ -363,8 +363,8 @@ convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M
  * code * scale; scale = max|row| / 127 over the D elements of a token's head).
  *
  * Positions, slots, page numbers, lengths and offsets are read on the device.
- * One outside its tensor is never followed: the token or row concerned is left
- * out and convrot_device_status reports it (bit 1).
+ * One outside its tensor is never followed, and convrot_device_status reports it
+ * (bit 1).  What it concerns is left out: each entry says what that is.
  * ------------------------------------------------------------------------ */
 
 /*
@@ -386,6 +386,8 @@ convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M
  * q_out      bf16 [tokens, q_heads, D]   out  may be q itself (same stride)
  * k_out      bf16 [tokens, kv_heads, D] or NULL  out  rotated k; may be k itself
  * k_cache, v_cache, k_scale, v_scale     in/out  only the slots' rows are written
+ * A token whose position is outside rope, or whose slot is past the cache, is
+ * left out: none of its rows is written.
  */
 convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                    const void* v, int64_t v_stride, int tokens, int q_heads,
@@ -408,6 +410,9 @@ convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* 
  * scale      > 0
  * out        bf16 [tokens, q_heads, D]  out  rows of no sequence are left as
  *            they were; out must not overlap an input
+ * A sequence whose offsets decrease or leave q, k or v is left out.  Offsets
+ * that go back and forth, so that the sequences are more than the rows can
+ * hold, leave out the whole call.
  */
 convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
                                         const void* v, int64_t v_stride, int tokens, int kv_tokens,
@@ -424,6 +429,9 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  * table      int32 [seqs, table_cols], rows table_stride apart  in  entries
  *            past a sequence's last page are not read
  * lens       int32 [seqs]  in   0 .. table_cols * page_size
+ *            A length outside that range counts as 0.  Keys of a page outside
+ *            the cache are left out of the sums; a sequence without a key that
+ *            can be read is 0.
  * out        bf16 [seqs, q_heads, D]  out
  * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte
  *            aligned, zero-filled before its first use; every call that

@@ -814,3 +814,48 @@ def test_decode_heads_do_not_touch_one_another(cr, Hq, Hkv, D, page, i8):
             cr.convrot_attention_prompt(*(x * 100 for x in p[:3]), torch.from_numpy(p[3]).cuda())
         assert torch.equal(cr.convrot_attention_decode(**c), want)
     assert cr.convrot_device_status() == 0
+
+
+# ------------------------------------------------------------------ pages that cannot be read
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("page", [16, 64])
+def test_decode_pages_that_cannot_be_read_are_left_out(cr, page, i8):
+    """Keys of a page outside the cache take no part; a sequence none of whose
+    pages can be read is 0, within one CTA's stretch and over many."""
+    for lens in ([40, 16, 9, 300], [9000], [1, 9000, 5]):
+        c = decode_case(11, lens, 4, 2, 64, page, i8)
+        good = check_decode(cr, c, lens)
+        for row in range(len(lens)):
+            d = dict(c, block_table=c["block_table"].clone())
+            d["block_table"][row] = -1
+            got = cr.convrot_attention_decode(**d)
+            assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+            assert not got[row].any(), "a sequence without a page that can be read"
+            keep = [i for i in range(len(lens)) if i != row]
+            assert torch.equal(got[keep], good[keep])
+    lens = [200]
+    c = decode_case(12, lens, 4, 2, 64, page, i8)
+    table = c["block_table"].clone()
+    table[0, 1] = 10 ** 6
+    got = f64(cr.convrot_attention_decode(**dict(c, block_table=table)))
+    assert cr.convrot_device_status() == 2
+    see = np.ones((1, 200), bool)
+    see[0, page:2 * page] = False
+    s = [None if c.get(x) is None else c[x].cpu().double().numpy() for x in ("k_scale", "v_scale")]
+    rows = c["block_table"].cpu().numpy()[0]
+    k, v = ref.cache_rows(f64(c["k_cache"]), s[0], rows, 200), ref.cache_rows(f64(c["v_cache"]), s[1], rows, 200)
+    at = np.arange(200)
+    for h in range(4):
+        vs = None if s[1] is None else s[1][rows[at // page], :, at % page][:, h // 2]
+        o, tol = ref.attention(f64(c["q"])[0, h][None], k[:, h // 2], v[:, h // 2], 64 ** -0.5, see, vs)
+        within(got[0, h], o[0], tol[0], f"head {h}")
+
+
+def test_decode_only_scores_of_minus_infinity(cr):
+    """Keys that are there and all score -inf: the softmax has no value, and
+    the row is NaN, not the 0 of a sequence without keys."""
+    for lens in ([40], [9000]):
+        c = decode_case(13, lens, 2, 1, 64, 16, False, fill=0.0)
+        c["q"][..., 0] = 300.0
+        c["k_cache"][..., 0] = -3e38
+        assert torch.isnan(cr.convrot_attention_decode(**c)).all()

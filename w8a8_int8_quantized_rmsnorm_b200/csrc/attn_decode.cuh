@@ -43,7 +43,9 @@
 // for a table entry that the stream itself had driven out of L2.
 //
 // Rows past a sequence's end are never used: their scores are replaced, their
-// values' registers cleared, pages behind the last one not fetched.
+// values' registers cleared, pages behind the last one not fetched.  Neither is
+// a page whose number is outside the cache; a sequence without a key that could
+// be read is 0, told from one whose scores are all -inf (NaN) by its maximum.
 #pragma once
 
 #include "attn_row.cuh"
@@ -84,6 +86,8 @@ struct DecodeBlock {
   int heads;            // query heads of the unit that there are
   int pad;
 };
+// The maximum of keys that all score -inf; -inf itself: there were no keys.
+constexpr float LOWEST = -3.402823466e38f;
 // begins / ends this CTA's stretch of the (seq, unit); no more blocks
 constexpr unsigned BLOCK_FIRST = 256, BLOCK_LAST = 512, BLOCK_END = 1024;
 
@@ -362,6 +366,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     float m[HL], l[HL];
     auto out_at = [&](int x, int k, int r) -> float& { return acc[I8 ? x : x / 2][k][I8 ? r : (x & 1) + 2 * r]; };
     uint32_t met = 0, parity = 0;
+    bool seen = false;  // this warp has met a key of the stretch
     // bounded rendezvous of the four compute warps
     auto rendezvous = [&]() -> bool {
       __syncwarp();
@@ -443,10 +448,12 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             for (int e = 0; e < (I8 ? 2 : 4); ++e) acc[n][k][e] = 0.f;
 #pragma unroll
         for (int x = 0; x < HL; ++x) m[x] = -INFINITY, l[x] = 0.f;
+        seen = false;
       }
       const int left = block_left - SLICE * warp;  // keys of this warp's share that exist
       const unsigned there = (flags >> (SLICE / 16 * warp)) & (I8 ? 3u : 1u);
       if (left > 0 && there) {
+        seen = true;
         const uint32_t kb = smem_addr(smem + s * SM::SLOT), vb = kb + SM::TILE;
         constexpr int NR = SLICE / 8;  // keys g + 8 r, r < NR, are this lane's
         float sc[HL][NR];              // their scores, times log2(e)
@@ -608,6 +615,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
       parity ^= 1u;
 #pragma unroll
       for (int x = 0; x < HL; ++x) {
+        if (seen) m[x] = fmaxf(m[x], LOWEST);
 #pragma unroll
         for (int o = 4; o < 32; o <<= 1) l[x] += __shfl_xor_sync(0xFFFFFFFFu, l[x], o);
         if (g == 0) {
@@ -650,14 +658,14 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         }
         return v;
       };
-      auto store = [&](int h, int d, float4 v, float sum) {
-        const float inv = b.left > 0 || sum > 0.f ? 1.f / sum : 0.f;  // a sequence without keys: 0
+      auto store = [&](int h, int d, float4 v, float top, float sum) {
+        const float inv = top == -INFINITY ? 0.f : 1.f / sum;  // a sequence without keys: 0
         *reinterpret_cast<uint2*>(out + h * D + d) = make_uint2(bf16x2(v.x * inv, v.y * inv), bf16x2(v.z * inv, v.w * inv));
       };
       if (b.n_parts == 1) {
         for (int x = threadIdx.x; x < qh * (D / 4); x += 128) {
           const int h = x / (D / 4), d = (x % (D / 4)) * 4;
-          store(h, d, joined(h, d), all[h * 2 + 1]);
+          store(h, d, joined(h, d), all[h * 2], all[h * 2 + 1]);
         }
         continue;
       }
@@ -717,7 +725,7 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             v.w = fmaf(y[p].w, fp, v.w);
           }
         }
-        store(h, d, v, sum);
+        store(h, d, v, top, sum);
       }
       if (!rendezvous()) break;
       for (int x = threadIdx.x; x < b.n_parts * (part_floats / 4); x += 128)  // as it was found

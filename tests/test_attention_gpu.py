@@ -787,7 +787,42 @@ def long_decode_case(seed, lens, Hq, Hkv, D, page, i8):
     return c
 
 
+def oracle_rows(c, lens, b, h):
+    """The oracle's (o, tol) of one head of one sequence."""
+    n, page = lens[b], c["k_cache"].shape[2]
+    kv = h // (c["q"].shape[1] // c["k_cache"].shape[1])
+    at = torch.arange(n, device="cuda")
+    where = (c["block_table"][b].long()[at // page], torch.full_like(at, kv), at % page)
+    k, v = (c[x][where].double().cpu().numpy() for x in ("k_cache", "v_cache"))
+    vs = None
+    if c.get("k_scale") is not None:
+        vs = c["v_scale"][where].double().cpu().numpy()
+        k, v = k * c["k_scale"][where].double().cpu().numpy()[:, None], v * vs[:, None]
+    o, tol = ref.attention(f64(c["q"])[b, h][None], k, v, c["q"].shape[2] ** -0.5, np.ones((1, n), bool), vs)
+    return o[0], tol[0]
+
+
 LONG = [(32, 8, 128, 16), (64, 8, 128, 48), (16, 4, 64, 64), (16, 2, 64, 128), (20, 1, 128, 16)]
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("Hq,Hkv,D,page", LONG)
+def test_decode_many_blocks_per_cta(cr, Hq, Hkv, D, page, i8):
+    """Stretches of dozens of blocks: every ring slot taken again and again,
+    several batches of pages per sequence, references raised on the way."""
+    rng = np.random.default_rng(Hq + D)
+    seqs = 400 // Hkv
+    lens = [int(n) for n in rng.integers(1, 6000, seqs)]
+    lens[:3] = [6000, 1, 5953]
+    c = long_decode_case(seqs, lens, Hq, Hkv, D, page, i8)
+    got = cr.convrot_attention_decode(**c)
+    assert cr.convrot_device_status() == 0
+    got = f64(got)
+    assert np.isfinite(got).all()
+    for b in [0, 1, 2, seqs - 1] + [int(x) for x in rng.integers(3, seqs, 12)]:
+        for h in {0, Hq - 1, int(rng.integers(Hq))}:
+            o, tol = oracle_rows(c, lens, b, h)
+            within(got[b, h], o, tol, f"sequence {b} head {h}")
 
 
 @pytest.mark.parametrize("i8", [False, True])
@@ -859,3 +894,36 @@ def test_decode_only_scores_of_minus_infinity(cr):
         c["q"][..., 0] = 300.0
         c["k_cache"][..., 0] = -3e38
         assert torch.isnan(cr.convrot_attention_decode(**c)).all()
+
+
+# ------------------------------------------------------------------ many units per CTA
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (32, 4, 64), (40, 8, 64), (8, 8, 128)])
+def test_prompt_many_units_per_cta(cr, Hq, Hkv, D, causal):
+    """Hundreds of units of one to eleven key tiles, so that CTAs take over one
+    unit after another: the same bits as each prompt's heads alone, where every
+    unit has a CTA of its own, and sampled rows within the oracle's bounds."""
+    group = Hq // Hkv
+    lens = [1333, 1, 700, 64, 65, 1025, 128, 300, 999, 17, 1280, 450]
+    if group == 1:
+        lens = lens * 3
+    q, k, v, cu, _ = prompt_case(90 + Hq, lens, lens, Hq, Hkv, D)
+    units = sum(-(-n // (2 * (128 // group))) for n in lens) * Hkv
+    assert units > 300
+    whole = cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda(), causal=causal)
+    for _ in range(3):
+        assert torch.equal(whole, cr.convrot_attention_prompt(q, k, v, torch.from_numpy(cu).cuda(), causal=causal))
+    for a, b in zip(cu[:12], cu[1:]):
+        one = torch.tensor([0, b - a], dtype=torch.int32).cuda()
+        for h in range(Hkv):
+            mine = slice(h * group, (h + 1) * group)
+            got = cr.convrot_attention_prompt(q[a:b, mine], k[a:b, h:h + 1], v[a:b, h:h + 1], one, causal=causal)
+            assert torch.equal(whole[a:b, mine], got)
+    assert cr.convrot_device_status() == 0
+    rng = np.random.default_rng(Hq)
+    for s in rng.integers(0, len(lens), 8):
+        a, n, h = int(cu[s]), lens[s], int(rng.integers(Hq))
+        i = int(rng.integers(n))
+        see = np.arange(n)[None] <= (i if causal else n)
+        o, tol = ref.attention(f64(q[a + i, h])[None], f64(k[a:a + n, h // group]), f64(v[a:a + n, h // group]), D ** -0.5, see)
+        within(f64(whole[a + i, h]), o[0], tol[0], f"sequence {s} row {i} head {h}")

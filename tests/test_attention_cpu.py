@@ -246,3 +246,24 @@ def test_decode_operands():
             v_scale=f32(5, 2))
     _raises("v_scale must be a torch.Tensor", f, q, cache.to(torch.int8), cache.to(torch.int8), table, lens,
             k_scale=f32(5, 2, 16))
+
+
+# ------------------------------------------------------------------ slots
+def test_slots_of_tokens_the_table_has_no_place_for():
+    """Indices outside the block table are not followed (on a GPU they would end
+    the process): padding is not stored, a token without a place is past every
+    cache, where the append leaves it out and reports it."""
+    cache = cr.PagedKVCache.__new__(cr.PagedKVCache)
+    cache.page_size = 16
+    table = torch.tensor([[3, 1], [0, -1]], dtype=torch.int32)
+
+    def slots(sequence, position, table=table):
+        return cache.slots(table, torch.tensor(sequence), torch.tensor(position, dtype=torch.int32)).tolist()
+
+    assert slots([0, 0, 0, 1, 1], [0, 15, 16, 5, 15]) == [48, 63, 16, 5, 15]
+    assert all(s < 0 for s in slots([1, 1, 0, 1, -1, -1], [16, 31, -1, -16, 0, 99]))
+    most = 2 ** 31 * 4096          # no cache has a slot so far
+    assert all(s >= most for s in slots([0, 1, 2, 7, 0], [32, 1 << 30, 0, 5, 2 ** 31 - 1]))
+    empty = torch.empty(2, 0, dtype=torch.int32)
+    assert [s >= most for s in slots([0, 1, 2], [0, 5, 0], empty)] == [True] * 3
+    assert slots([0, -1], [-1, 3], empty) == [-1, -1] and slots([], []) == []

@@ -927,3 +927,27 @@ def test_prompt_many_units_per_cta(cr, Hq, Hkv, D, causal):
         see = np.arange(n)[None] <= (i if causal else n)
         o, tol = ref.attention(f64(q[a + i, h])[None], f64(k[a:a + n, h // group]), f64(v[a:a + n, h // group]), D ** -0.5, see)
         within(f64(whole[a + i, h]), o[0], tol[0], f"sequence {s} row {i} head {h}")
+
+
+# ------------------------------------------------------------------ slots
+def test_append_at_slots_the_table_has_no_place_for(cr):
+    """Padding is not stored; a token past its sequence's pages is left out and
+    reported; the others are as ever."""
+    cache = cr.PagedKVCache(6, 2, 64, page_size=16)
+    table = torch.tensor([[4, 1], [0, -1]], dtype=torch.int32).cuda()
+    seq, pos = torch.tensor([0, 0, 1, 1, -1, 0]).cuda(), torch.tensor([0, 31, 3, 20, 5, 7], dtype=torch.int32).cuda()
+    c = append_case(14, 6, 4, 2, 64, 64, 16, False, False, rows=50)
+    c |= dict(k_cache=cache.k, v_cache=cache.v, positions=pos, slots=cache.slots(table, seq, pos))
+    before, q, k = run_append(cr, c)               # nothing to report: padding and a page that is not there
+    check_append(c, before, q, k)
+    pos = pos.clone()
+    pos[1], seq[2] = 32, 9
+    c |= dict(positions=pos, slots=cache.slots(table, seq, pos))
+    before = {n: t.clone() for n, t in c.items()}
+    q, k = torch.zeros_like(q), torch.zeros_like(k)
+    cr.convrot_rope_append(**c, q_out=q, k_out=k)
+    assert cr.convrot_device_status() == 2 and cr.convrot_device_status() == 0
+    assert not q[1:3].any() and not k[1:3].any()
+    keep = torch.tensor([0, 3, 4, 5])
+    pick = lambda d: {n: t[keep] if n in ("q", "k", "v", "positions", "slots") else t for n, t in d.items()}
+    check_append(pick(c), pick(before), q[keep], k[keep])

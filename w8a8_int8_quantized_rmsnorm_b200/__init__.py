@@ -757,6 +757,10 @@ def rope_table(rows: int, dim: int, theta: float = 1e6, device=None) -> torch.Te
     return torch.cat([angle.cos(), angle.sin()], 1).float()
 
 
+# A slot past every cache.
+NO_PLACE = 1 << 62
+
+
 class PagedKVCache:
     """One layer's keys and values in pages of page_size tokens: bf16, or int8
     with one fp32 scale per token and head.  Which sequence owns which page is
@@ -772,10 +776,18 @@ class PagedKVCache:
 
     def slots(self, block_table: torch.Tensor, sequence: torch.Tensor, position: torch.Tensor) -> torch.Tensor:
         """Slots (int64) of tokens at `position` of rows `sequence` of the block
-        table.  A page that is not there (negative) gives a negative slot: such
-        a token is not stored."""
-        page = block_table[sequence.long(), position.long() // self.page_size].long()
-        return page * self.page_size + position % self.page_size
+        table.  A token that is not to be stored has a negative slot: its page is
+        not there (negative), or its sequence or position is negative (padding).
+        One that the table has no place for has a slot past every cache, which
+        convrot_rope_append leaves out and reports."""
+        rows, cols = block_table.shape
+        sequence, position = sequence.long(), position.long()
+        column = position // self.page_size
+        slot = torch.full_like(position, NO_PLACE)
+        if rows and cols:
+            page = block_table[sequence.clamp(0, rows - 1), column.clamp(0, cols - 1)].long()
+            slot = torch.where((sequence < rows) & (column < cols), page * self.page_size + position % self.page_size, slot)
+        return torch.where((sequence < 0) | (position < 0), -1, slot)
 
 
 class ConvRotAttention:

@@ -386,6 +386,9 @@ convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M
  * q_out      bf16 [tokens, q_heads, D]   out  may be q itself (same stride)
  * k_out      bf16 [tokens, kv_heads, D] or NULL  out  rotated k; may be k itself
  * k_cache, v_cache, k_scale, v_scale     in/out  only the slots' rows are written
+ * Outputs that share memory with q, k, v or one another in any other way, and a
+ * k_cache that overlaps v_cache, are refused (CONVROT_ERR_UNSUPPORTED).  Column
+ * views of one buffer share none.
  * A token whose position is outside rope, or whose slot is past the cache, is
  * left out: none of its rows is written.
  */
@@ -409,7 +412,7 @@ convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* 
  *            first rows in q and in k, v (the same pointer when they agree)
  * scale      > 0
  * out        bf16 [tokens, q_heads, D]  out  rows of no sequence are left as
- *            they were; out must not overlap an input
+ *            they were; one that shares memory with q, k or v is refused
  * A sequence whose offsets decrease or leave q, k or v is left out.  Offsets
  * that go back and forth, so that the sequences are more than the rows can
  * hold, leave out the whole call.
@@ -432,7 +435,8 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  *            A length outside that range counts as 0.  Keys of a page outside
  *            the cache are left out of the sums; a sequence without a key that
  *            can be read is 0.
- * out        bf16 [seqs, q_heads, D]  out
+ * out        bf16 [seqs, q_heads, D]  out  may be q itself (same stride); one that
+ *            shares memory with q in another way is refused
  * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte
  *            aligned, zero-filled before its first use; every call that
  *            completes leaves it zero, so the linears may share it.  (This

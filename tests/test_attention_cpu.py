@@ -267,3 +267,49 @@ def test_slots_of_tokens_the_table_has_no_place_for():
     empty = torch.empty(2, 0, dtype=torch.int32)
     assert [s >= most for s in slots([0, 1, 2], [0, 5, 0], empty)] == [True] * 3
     assert slots([0, -1], [-1, 3], empty) == [-1, -1] and slots([], []) == []
+
+
+# ------------------------------------------------------------------ results on inputs
+def test_decode_results_on_queries(lib):
+    """In place or apart; anything between is refused.  Every arrangement of two
+    to five rows against their bytes one by one.  (The calls have no workspace,
+    so that none of them launches.)"""
+    rng = np.random.default_rng(0)
+    width, kinds = 2 * 128, set()
+    for _ in range(3000):
+        n = int(rng.integers(1, 6))
+        sq, so = (int(x) for x in rng.choice([128, 136, 264, 384, 520], 2))
+        if rng.random() < 0.5:
+            so = sq
+        q = 1 << 20
+        out = q + 16 * int(rng.integers(-150, 150)) if rng.random() < 0.9 else q
+        taken = [set().union(*(range(p + 2 * s * i, p + 2 * s * i + width, 16) for i in range(n))) for p, s in ((q, sq), (out, so))]
+        shares = bool(taken[0] & taken[1]) and not (q == out and (sq == so or n == 1))
+        st = _decode(lib, q=_p(q), qs=sq, out=_p(out), os=so, seqs=n, hq=1, hkv=1)
+        assert (st == 4) == shares and st in (4, 5, 7), (n, sq, so, out - q)
+        kinds.add((shares, sq == so, q < out))
+    assert len(kinds) == 8
+
+
+def test_append_results_on_inputs(lib):
+    """q_out may be q and k_out may be k; nothing else may share memory."""
+    at = dict(q=0x100000, k=0x200000, v=0x300000, qo=0x400000, ko=0x500000, kc=0x600000, vc=0x700000)
+    ok = {n: _p(p) for n, p in at.items()} | dict(kos=128)
+
+    def status(**kw):
+        return _append(lib, **(ok | kw))
+
+    for out, stride, inputs in (("qo", "qos", ("k", "v", "ko")), ("ko", "kos", ("q", "v", "qo"))):
+        for name in inputs:
+            assert status(**{out: _p(at[name])}) == 4 and status(**{out: _p(at[name] + 16)}) == 4
+    assert status(qo=_p(at["q"] + 16)) == 4 and status(qo=_p(at["q"]), qos=520) == 4
+    assert status(ko=_p(at["k"] + 16)) == 4 and status(ko=_p(at["k"]), kos=136) == 4
+    assert status(vc=_p(at["kc"])) == 4 and status(vc=_p(at["kc"] + 3 * 16 * 128 * 2 - 16)) == 4
+    scales = dict(sk=_p(0x800000), sv=_p(0x800000))
+    assert status(**scales) == 4 and status(sk=_p(0x800000), sv=_p(0x800000 + 3 * 16 * 4 - 16)) == 4
+
+
+def test_prompt_results_on_inputs(lib):
+    for name, wide in (("q", 512), ("k", 128), ("v", 128)):
+        for off in (16, -16, 4 * 2 * wide - 16, 16 - 4 * 2 * 512):       # four rows of each, four of the result
+            assert _prompt(lib, **{name: _p(0x20000 - off)}) == 4, (name, off)

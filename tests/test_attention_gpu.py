@@ -951,3 +951,33 @@ def test_append_at_slots_the_table_has_no_place_for(cr):
     keep = torch.tensor([0, 3, 4, 5])
     pick = lambda d: {n: t[keep] if n in ("q", "k", "v", "positions", "slots") else t for n, t in d.items()}
     check_append(pick(c), pick(before), q[keep], k[keep])
+
+
+# ------------------------------------------------------------------ results beside inputs
+def test_results_beside_and_in_place_of_inputs(cr):
+    """Results in columns of the buffer that holds the inputs, and a decode in
+    place: the same bits as results of their own, nothing else touched."""
+    T, Hq, Hkv, D = 150, 8, 2, 64
+    wide = randn(15, T, (2 * Hq + 2 * Hkv) * D)
+    q, k, v, out = (x.view(T, -1, D) for x in wide.split([Hq * D, Hkv * D, Hkv * D, Hq * D], 1))
+    before = wide.clone()
+    cu = torch.tensor([0, 90, T], dtype=torch.int32).cuda()
+    want = cr.convrot_attention_prompt(q, k, v, cu)
+    assert cr.convrot_attention_prompt(q, k, v, cu, out=out).data_ptr() == out.data_ptr()
+    assert torch.equal(out, want) and torch.equal(wide[:, :(Hq + 2 * Hkv) * D], before[:, :(Hq + 2 * Hkv) * D])
+    for bad in (q, wide[:, D:(Hq + 1) * D].view(T, Hq, D), wide[:, (Hq + 1) * D:(2 * Hq + 1) * D].view(T, Hq, D)):
+        with pytest.raises(cr.ConvRotError, match="UNSUPPORTED"):
+            cr.convrot_attention_prompt(q, k, v, cu, out=bad)
+    c = append_case(16, T, Hq, Hkv, D, D, 16, False, True)
+    with pytest.raises(cr.ConvRotError, match="UNSUPPORTED"):
+        cr.convrot_rope_append(**c, q_out=c["q"], k_out=c["q"][:, 1:1 + Hkv])
+    with pytest.raises(cr.ConvRotError, match="UNSUPPORTED"):
+        cr.convrot_rope_append(**(c | dict(v_cache=c["k_cache"])))
+    lens = [300, 4, 0, 7000]
+    d = decode_case(17, lens, Hq, Hkv, D, 16, False)
+    want = cr.convrot_attention_decode(**d)
+    assert cr.convrot_attention_decode(**d, out=d["q"]) is d["q"] and torch.equal(d["q"], want)
+    with pytest.raises(cr.ConvRotError, match="UNSUPPORTED"):
+        cr.convrot_attention_decode(**(d | dict(q=d["q"][:3], block_table=d["block_table"][:3], seq_lens=d["seq_lens"][:3])),
+                                    out=d["q"][1:])
+    assert cr.convrot_device_status() == 0

@@ -20,6 +20,45 @@ bool stride_ok(int64_t stride, int heads, int D, int rows) {
   return stride % 8 == 0 && stride <= kMaxStride && (rows <= 1 || stride >= static_cast<int64_t>(heads) * D);
 }
 
+// A tensor's memory: rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+  uintptr_t at;
+  int64_t stride, width, rows;
+  uintptr_t end() const { return at + static_cast<uintptr_t>((rows - 1) * stride + width); }
+};
+Rows head_rows(const void* p, int64_t stride, int heads, int D, int rows) {
+  const int64_t width = static_cast<int64_t>(heads) * D * 2;
+  return {reinterpret_cast<uintptr_t>(p), rows > 1 ? stride * 2 : width, width, p ? rows : 0};
+}
+Rows piece(const void* p, int64_t bytes) { return {reinterpret_cast<uintptr_t>(p), bytes, bytes, p && bytes > 0 ? 1 : 0}; }
+
+// Whether two tensors share a byte.  Column views of one buffer lie between one
+// another's rows and share none.
+bool overlap(const Rows& a, const Rows& b) {
+  if (a.rows == 0 || b.rows == 0 || a.end() <= b.at || b.end() <= a.at) return false;
+  if (a.rows == 1 && b.rows == 1) return true;
+  const int64_t apart = static_cast<int64_t>(b.at - a.at);
+  if (a.rows == 1 || b.rows == 1 || a.stride == b.stride) {
+    // rows i and j meet where -b.width < apart + (j - i) stride < a.width
+    const int64_t stride = a.rows > 1 ? a.stride : b.stride, low = -b.width - apart;
+    int64_t k = low / stride - (low % stride < 0 ? 1 : 0) + 1;  // the first k with low < k stride
+    k = std::max(k, -(a.rows - 1));
+    return k <= b.rows - 1 && apart + k * stride < a.width;
+  }
+  for (int64_t i = 0, j = 0; i < a.rows && j < b.rows;) {
+    const int64_t x = i * a.stride, y = apart + j * b.stride;
+    if (x + a.width <= y)
+      ++i;
+    else if (y + b.width <= x)
+      ++j;
+    else
+      return true;
+  }
+  return false;
+}
+// The one way in which a result may lie on an input: in its place.
+bool in_place(const Rows& a, const Rows& b) { return a.at == b.at && a.stride == b.stride && a.width == b.width; }
+
 convrot_status run_append(const AppendArgs& args, int D, bool int8, cudaStream_t st) {
   const DeviceInfo d = current_device();
   if (d.device < 0 || d.sms <= 0) return CONVROT_ERR_CUDA;
@@ -176,6 +215,18 @@ convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* 
       !aligned(v_cache, 16) || !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(q_norm, 16) ||
       !aligned(k_norm, 16))
     return CONVROT_ERR_ALIGN;
+  const Rows rq = head_rows(q, q_stride, q_heads, head_dim, tokens), rk = head_rows(k, k_stride, kv_heads, head_dim, tokens),
+             rv = head_rows(v, v_stride, kv_heads, head_dim, tokens),
+             rqo = head_rows(q_out, q_out_stride, q_heads, head_dim, tokens),
+             rko = head_rows(k_out, k_out_stride, kv_heads, head_dim, tokens);
+  if ((overlap(rqo, rq) && !in_place(rqo, rq)) || overlap(rqo, rk) || overlap(rqo, rv) || overlap(rqo, rko) ||
+      (overlap(rko, rk) && !in_place(rko, rk)) || overlap(rko, rq) || overlap(rko, rv))
+    return CONVROT_ERR_UNSUPPORTED;  // another warp may have yet to read what lies there
+  const int64_t lines = static_cast<int64_t>(pages) * kv_heads * page_size;
+  const int64_t bytes = lines * head_dim * (k_scale ? 1 : 2);
+  if (overlap(piece(k_cache, bytes), piece(v_cache, bytes)) ||
+      overlap(piece(k_scale, lines * 4), piece(v_scale, lines * 4)))
+    return CONVROT_ERR_UNSUPPORTED;
   AppendArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -225,6 +276,11 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
   if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(out, 16) || !aligned(cu_q, 4) ||
       !aligned(cu_k, 4))
     return CONVROT_ERR_ALIGN;
+  const Rows ro = head_rows(out, out_stride, q_heads, head_dim, tokens);
+  if (overlap(ro, head_rows(q, q_stride, q_heads, head_dim, tokens)) ||
+      overlap(ro, head_rows(k, k_stride, kv_heads, head_dim, kv_tokens)) ||
+      overlap(ro, head_rows(v, v_stride, kv_heads, head_dim, kv_tokens)))
+    return CONVROT_ERR_UNSUPPORTED;
   PromptArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.k = static_cast<const uint16_t*>(k);
@@ -274,6 +330,9 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   if (!aligned(workspace, 256) || !aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
       !aligned(k_scale, 16) || !aligned(v_scale, 16) || !aligned(table, 4) || !aligned(lens, 4))
     return CONVROT_ERR_ALIGN;
+  // (a row's query is read before its result is written, by whichever CTA)
+  const Rows rq = head_rows(q, q_stride, q_heads, head_dim, seqs), ro = head_rows(out, out_stride, q_heads, head_dim, seqs);
+  if (overlap(ro, rq) && !in_place(ro, rq)) return CONVROT_ERR_UNSUPPORTED;
   DecodeArgs a{};
   a.q = static_cast<const uint16_t*>(q);
   a.q_stride = q_stride;

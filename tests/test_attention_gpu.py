@@ -981,3 +981,55 @@ def test_results_beside_and_in_place_of_inputs(cr):
         cr.convrot_attention_decode(**(d | dict(q=d["q"][:3], block_table=d["block_table"][:3], seq_lens=d["seq_lens"][:3])),
                                     out=d["q"][1:])
     assert cr.convrot_device_status() == 0
+
+
+# ------------------------------------------------------------------ workspaces and graphs
+def workspace_calls(cr, i):
+    """A call that takes a Workspace, and one that needs a larger one."""
+    if i == 2:
+        g = torch.Generator().manual_seed(3)
+        X, W = (torch.randint(-127, 128, (n, 12288), generator=g, dtype=torch.int16).to(torch.int8).cuda() for n in (768, 6400))
+        return (lambda ws: cr.convrot_int8_gemm_s32(X[:16].contiguous(), W[:4096].contiguous(), workspace=ws),
+                lambda ws: cr.convrot_int8_gemm_s32(X, W, workspace=ws))
+    small, big = (decode_case(100 + h, [3000, 70], h, 1, 128, 16, bool(i)) for h in (2, 16))
+    return lambda ws: cr.convrot_attention_decode(**small, workspace=ws), lambda ws: cr.convrot_attention_decode(**big, workspace=ws)
+
+
+@pytest.mark.parametrize("i", range(3))
+def test_workspace_captured_before_any_call(cr, i):
+    """Eager calls between a capture and its first replay, a second graph
+    replayed before the first, and replays after either."""
+    f, _ = workspace_calls(cr, i)
+    want = f(cr.Workspace())
+    ws, graphs, outs = cr.Workspace(), [], []
+    for _ in range(2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            outs.append(f(ws))
+    for _ in range(2):
+        assert torch.equal(f(ws), want)
+        for g, o in reversed(list(zip(graphs, outs))):
+            o.zero_()
+            g.replay()
+            assert torch.equal(o, want)
+    assert cr.convrot_device_status() == 0
+
+
+@pytest.mark.parametrize("i", range(3))
+def test_workspace_that_grows_behind_a_captured_graph(cr, i):
+    """The graph goes on using the buffer that it was captured with."""
+    f, larger = workspace_calls(cr, i)
+    ws = cr.Workspace()
+    want = f(ws)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = f(ws)
+    size = ws.buf.numel()
+    want_larger = larger(ws)
+    assert ws.buf.numel() > size
+    taken = [torch.full((size,), 0x55, dtype=torch.uint8, device="cuda") for _ in range(8)]   # what was freed, if it was
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        assert torch.equal(out, want) and torch.equal(larger(ws), want_larger)
+    assert all((t == 0x55).all() for t in taken) and cr.convrot_device_status() == 0

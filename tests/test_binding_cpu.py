@@ -95,3 +95,40 @@ def test_workspace_is_cleared_after_a_reported_timeout(monkeypatch):
     ws.buf.fill_(1)
     ws.get(64)                       # cleared once per report, not on every call
     assert int(ws.buf.sum()) == 64
+
+
+def test_workspace_and_captured_graphs(monkeypatch):
+    """A fill recorded into a graph runs at its replays only: a buffer made
+    during a capture is the graph's own, never one that other calls (another
+    graph's, eager ones) take for clear.  And a buffer that a graph uses is not
+    freed when the Workspace grows.  (CPU buffers; whether a capture is under
+    way is given directly.)"""
+    import weakref
+
+    capturing = [True]
+    monkeypatch.setattr(cr, "_capturing", lambda device: capturing[0], raising=False)
+    ws = cr.Workspace.__new__(cr.Workspace)
+    ws.device, ws.buf, ws.epoch = torch.device("cpu"), None, cr._timeouts_reported
+    first, n = ws.get(64)
+    assert n == 64 and ws.buf is None
+    second, _ = ws.get(64)                       # another graph
+    capturing[0] = False
+    eager, n = ws.get(64)
+    assert n == 64 and len({first, second, eager}) >= 2 and eager != second
+    capturing[0] = True
+    assert ws.get(48) == (eager, 64)             # there and clear: the graph uses it
+    old = weakref.ref(ws.buf)
+    assert ws.get(128)[0] != eager and ws.buf is old()   # too small: the graph's own
+    capturing[0] = False
+    assert ws.get(64) == (eager, 64)
+    assert ws.get(128) != (eager, 128) and old() is not None and old().data_ptr() == eager
+    grown = weakref.ref(ws.buf)                  # no graph uses this one
+    ws.get(256)
+    assert grown() is None and old() is not None
+    ws.buf.fill_(7)
+    cr._note_status(6)
+    capturing[0] = True
+    assert ws.get(256)[0] != ws.buf.data_ptr()   # not clear: not for a graph
+    capturing[0] = False
+    ws.get(256)
+    assert int(ws.buf.sum()) == 0

@@ -200,6 +200,10 @@ def convrot_linear_workspace_bytes(M: int, N: int, K: int, weight_bits: int = 8)
     return int(lib().convrot_linear_workspace_bytes(M, N, K, weight_bits))
 
 
+def _capturing(device: torch.device) -> bool:
+    return device.type == "cuda" and torch.cuda.is_current_stream_capturing()
+
+
 class Workspace:
     """Device workspace for the GEMM's split tiles, grown on demand.
 
@@ -208,8 +212,17 @@ class Workspace:
     convrot_device_status has reported a device timeout (an aborted call may
     leave partial sums behind) it is zero-filled again before its next use.
     One Workspace must not be used by calls that run concurrently on
-    different streams.
+    different streams, replays of captured graphs among them.
+
+    A call captured into a graph takes the buffer if it is there, large enough
+    and clear by then, and the buffer stays in place for the graph's replays
+    when the Workspace grows.  Otherwise (no call has run before the capture)
+    it takes one of the graph's own, which every replay clears.
     """
+
+    lent = False    # self.buf is in use by a captured graph
+    kept = ()       # smaller buffers that are
+    own = None      # the graph's own buffer that was handed out last
 
     def __init__(self, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None else device)
@@ -219,7 +232,17 @@ class Workspace:
     def get(self, nbytes: int) -> Tuple[Optional[int], int]:
         if nbytes == 0:
             return None, 0
-        if self.buf is None or self.buf.numel() < nbytes:
+        short = self.buf is None or self.buf.numel() < nbytes
+        if _capturing(self.device):
+            if not short and self.epoch == _timeouts_reported:
+                self.lent = True
+                return self.buf.data_ptr(), self.buf.numel()
+            # (a fill recorded here runs at a replay, not now)
+            self.own = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            return self.own.data_ptr(), nbytes
+        if short:
+            if self.lent:
+                self.kept, self.lent = (*self.kept, self.buf), False
             self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
             self.epoch = _timeouts_reported
         elif self.epoch != _timeouts_reported:

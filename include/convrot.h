@@ -410,7 +410,7 @@ convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* 
  * q [tokens, q_heads, D]; k, v [kv_tokens, kv_heads, D]  in
  * cu_q, cu_k int32 [seqs + 1]  in   non-decreasing offsets of the sequences'
  *            first rows in q and in k, v (the same pointer when they agree)
- * scale      > 0
+ * scale      > 0, and finite times log2(e)
  * out        bf16 [tokens, q_heads, D]  out  rows of no sequence are left as
  *            they were; one that shares memory with q, k or v is refused
  * A sequence whose offsets decrease or leave q, k or v is left out.  Offsets
@@ -435,6 +435,7 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  *            A length outside that range counts as 0.  Keys of a page outside
  *            the cache are left out of the sums; a sequence without a key that
  *            can be read is 0.
+ * scale      as above
  * out        bf16 [seqs, q_heads, D]  out  may be q itself (same stride); one that
  *            shares memory with q in another way is refused
  * workspace  convrot_attention_decode_workspace_bytes(...) bytes, 256-byte

@@ -313,3 +313,13 @@ def test_prompt_results_on_inputs(lib):
     for name, wide in (("q", 512), ("k", 128), ("v", 128)):
         for off in (16, -16, 4 * 2 * wide - 16, 16 - 4 * 2 * 512):       # four rows of each, four of the result
             assert _prompt(lib, **{name: _p(0x20000 - off)}) == 4, (name, off)
+
+
+# ------------------------------------------------------------------ scales
+def test_scales_that_leave_fp32(lib):
+    """scores are held times log2(e): a scale that overflows by that would make
+    every result NaN."""
+    most = 3.4028234663852886e38
+    for scale in (most, most / 1.4426):
+        assert _prompt(lib, scale=scale) == 2 and _decode(lib, scale=scale) == 2
+    assert _decode(lib, scale=most / 1.443, out=_p(0x20000)) in (5, 7)      # (without a workspace: no launch)

@@ -266,7 +266,7 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
   if (tokens < 0 || kv_tokens < 0 || seqs < 0 || !heads_ok(q_heads, kv_heads)) return CONVROT_ERR_SHAPE;
   if (head_dim != 64 && head_dim != 128) return CONVROT_ERR_UNSUPPORTED;
   if (tokens > (1 << 24) || kv_tokens > (1 << 24) || seqs > (1 << 24)) return CONVROT_ERR_SHAPE;
-  if (!(scale > 0.f) || !(scale < INFINITY)) return CONVROT_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale * LOG2E < INFINITY)) return CONVROT_ERR_SHAPE;  // the kernels' scores are powers of two
   if (!stride_ok(q_stride, q_heads, head_dim, tokens) || !stride_ok(k_stride, kv_heads, head_dim, kv_tokens) ||
       !stride_ok(v_stride, kv_heads, head_dim, kv_tokens) || !stride_ok(out_stride, q_heads, head_dim, tokens))
     return CONVROT_ERR_SHAPE;
@@ -320,7 +320,7 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   if (seqs > (1 << 24) || pages < 0 || page_size < 1 || page_size > kMaxPage || page_size % 16 || table_cols < 0)
     return CONVROT_ERR_SHAPE;
   if (seqs > 1 && table_stride < table_cols) return CONVROT_ERR_SHAPE;
-  if (!(scale > 0.f) || !(scale < INFINITY)) return CONVROT_ERR_SHAPE;
+  if (!(scale > 0.f) || !(scale * LOG2E < INFINITY)) return CONVROT_ERR_SHAPE;  // the kernels' scores are powers of two
   if (!stride_ok(q_stride, q_heads, head_dim, seqs) || !stride_ok(out_stride, q_heads, head_dim, seqs))
     return CONVROT_ERR_SHAPE;
   if (seqs == 0) return CONVROT_OK;

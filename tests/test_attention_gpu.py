@@ -1033,3 +1033,11 @@ def test_workspace_that_grows_behind_a_captured_graph(cr, i):
         g.replay()
         assert torch.equal(out, want) and torch.equal(larger(ws), want_larger)
     assert all((t == 0x55).all() for t in taken) and cr.convrot_device_status() == 0
+
+
+def test_decode_refuses_a_workspace_of_another_device(cr):
+    c = decode_case(52, [70], 8, 2, 128, 16, False)
+    ws = cr.Workspace()
+    ws.device = torch.device("cuda", 1)
+    with pytest.raises(ValueError, match="the workspace is on cuda:1"):
+        cr.convrot_attention_decode(**c, workspace=ws)

@@ -132,3 +132,11 @@ def test_workspace_and_captured_graphs(monkeypatch):
     capturing[0] = False
     ws.get(256)
     assert int(ws.buf.sum()) == 0
+
+
+def test_workspace_of_another_device_is_refused():
+    """Its memory would be written by a kernel of this device."""
+    ws = cr.Workspace.__new__(cr.Workspace)
+    ws.device, ws.buf, ws.epoch = torch.device("cuda", 1), None, cr._timeouts_reported
+    with pytest.raises(ValueError, match="the workspace is on cuda:1, the operands are on cuda:0"):
+        cr._workspace(torch.device("cuda", 0), 64, ws)

@@ -254,13 +254,19 @@ class Workspace:
 _default_ws = {}
 
 
+def _workspace_on(index: int, ws: Workspace) -> Workspace:
+    if ws.device.index != index:
+        raise ValueError(f"the workspace is on {ws.device}, the operands are on cuda:{index}")
+    return ws
+
+
 def _workspace(dev: torch.device, nbytes: int, ws: Optional[Workspace]):
     if ws is None:
         key = (dev.index, torch.cuda.current_stream(dev).cuda_stream)
         ws = _default_ws.get(key)
         if ws is None:
             ws = _default_ws[key] = Workspace(dev.index)
-    p, n = ws.get(nbytes)
+    p, n = _workspace_on(dev.index, ws).get(nbytes)
     return (ctypes.c_void_p(p) if p else None), n
 
 
@@ -614,6 +620,7 @@ def convrot_attention_decode(q, k_cache, v_cache, block_table, seq_lens, *, k_sc
         workspace = _default_ws.get((dev, stream)) or _default_ws.setdefault((dev, stream), Workspace(dev))
         capturing = torch.cuda.is_current_stream_capturing()
     else:
+        _workspace_on(dev, workspace)
         capturing = False
     need = _decode_ws_bytes.get((dev, Hq, Hkv, D))
     if need is None and B:

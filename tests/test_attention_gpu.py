@@ -1041,3 +1041,26 @@ def test_decode_refuses_a_workspace_of_another_device(cr):
     ws.device = torch.device("cuda", 1)
     with pytest.raises(ValueError, match="the workspace is on cuda:1"):
         cr.convrot_attention_decode(**c, workspace=ws)
+
+
+# ------------------------------------------------------------------ values near the end of fp32
+def test_decode_int8_values_near_the_end_of_the_range(cr):
+    """A key whose probability, against a reference 2^7.5 below its score, times
+    its value's scale lies above 2^126: its share of the result is there."""
+    seqs, n, page, D = 700, 256, 16, 64        # two blocks each, several sequences to a CTA
+    k, v = (torch.zeros(n // page, 1, page, D, dtype=torch.int8) for _ in range(2))
+    ks, vs = torch.full((n // page, 1, page), 1e-3), torch.full((n // page, 1, page), 1e30)
+    at = 200 // page, 0, 200 % page
+    k[at][0], ks[at] = 127, 7.5 * np.log(2) / 127
+    v[at], vs[at] = 1, 6e35
+    v[at][0] = 127                             # this element's sum itself leaves fp32
+    q = torch.zeros(seqs, 1, D, dtype=torch.bfloat16)
+    q[..., 0] = 1
+    table = torch.arange(n // page, dtype=torch.int32).repeat(seqs, 1)
+    got = cr.convrot_attention_decode(q.cuda(), k.cuda(), v.cuda(), table.cuda(), torch.full((seqs,), n, dtype=torch.int32).cuda(),
+                                      k_scale=ks.cuda(), v_scale=vs.cuda(), scale=1.0)
+    rows = [x.double().numpy().reshape(n, D) * s.double().numpy().reshape(n, 1) for x, s in ((k, ks), (v, vs))]
+    o, tol = ref.attention(f64(q[0]), rows[0], rows[1], 1.0, np.ones((1, n), bool), vs.double().numpy().reshape(n))
+    assert o[0, 1] > 2e35
+    for b in range(seqs):
+        within(f64(got)[b, 0, 1:], o[0, 1:], tol[0, 1:], f"sequence {b}")

@@ -545,8 +545,9 @@ decode_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             float top = max_nan(max_nan(p[x][0], p[x][1]), max_nan(p[x][2], p[x][3]));
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = max_nan(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            // (scaled up first where 1 / top would overflow)
-            const float up = top < 1e-30f ? 0x1p64f : 1.f, inv = top > 0.f ? __fdividef(32512.f, top * up) : 0.f;
+            // (scaled towards 1 first, by a power of two: 1 / top may overflow, and
+            // the fast division is 0 for divisors above 2^126)
+            const float up = top < 1.f ? 0x1p64f : 0x1p-64f, inv = top > 0.f ? __fdividef(32512.f, top * up) : 0.f;
             ps[x] = top * (1.f / 32512.f);
             uint32_t mv[4];
 #pragma unroll

@@ -121,10 +121,9 @@ def test_workspace_and_captured_graphs(monkeypatch):
     assert ws.get(128)[0] != eager and ws.buf is old()   # too small: the graph's own
     capturing[0] = False
     assert ws.get(64) == (eager, 64)
-    assert ws.get(128) != (eager, 128) and old() is not None and old().data_ptr() == eager
-    grown = weakref.ref(ws.buf)                  # no graph uses this one
-    ws.get(256)
-    assert grown() is None and old() is not None
+    p, n = ws.get(65)                            # (twice as large: what is kept stays small)
+    assert p != eager and n == 128 and old() is not None and old().data_ptr() == eager
+    assert ws.get(256)[1] == 256 and old() is not None
     ws.buf.fill_(7)
     cr._note_status(6)
     capturing[0] = True

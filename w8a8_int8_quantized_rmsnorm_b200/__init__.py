@@ -215,13 +215,13 @@ class Workspace:
     different streams, replays of captured graphs among them.
 
     A call captured into a graph takes the buffer if it is there, large enough
-    and clear by then, and the buffer stays in place for the graph's replays
-    when the Workspace grows.  Otherwise (no call has run before the capture)
-    it takes one of the graph's own, which every replay clears.
+    and clear by then.  Otherwise (no call has run before the capture) it takes
+    one of the graph's own, which every replay clears.  When the Workspace grows,
+    at least to twice its size, the buffers before stay: captured graphs may go
+    on using them.
     """
 
-    lent = False    # self.buf is in use by a captured graph
-    kept = ()       # smaller buffers that are
+    kept = ()       # the buffers before self.buf
     own = None      # the graph's own buffer that was handed out last
 
     def __init__(self, device=None):
@@ -233,20 +233,17 @@ class Workspace:
         if nbytes == 0:
             return None, 0
         short = self.buf is None or self.buf.numel() < nbytes
-        if _capturing(self.device):
-            if not short and self.epoch == _timeouts_reported:
-                self.lent = True
-                return self.buf.data_ptr(), self.buf.numel()
-            # (a fill recorded here runs at a replay, not now)
-            self.own = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            return self.own.data_ptr(), nbytes
-        if short:
-            if self.lent:
-                self.kept, self.lent = (*self.kept, self.buf), False
-            self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-            self.epoch = _timeouts_reported
-        elif self.epoch != _timeouts_reported:
-            self.buf.zero_()
+        if short or self.epoch != _timeouts_reported:
+            if _capturing(self.device):  # (a fill recorded here runs at the replays, not now)
+                self.own = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+                return self.own.data_ptr(), nbytes
+            if short:
+                if self.buf is not None:
+                    self.kept = (*self.kept, self.buf)
+                    nbytes = max(nbytes, 2 * self.buf.numel())
+                self.buf = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+            else:
+                self.buf.zero_()
             self.epoch = _timeouts_reported
         return self.buf.data_ptr(), self.buf.numel()
 

@@ -1064,3 +1064,108 @@ def test_decode_int8_values_near_the_end_of_the_range(cr):
     assert o[0, 1] > 2e35
     for b in range(seqs):
         within(f64(got)[b, 0, 1:], o[0, 1:], tol[0, 1:], f"sequence {b}")
+
+
+# ------------------------------------------------------------------ the block, captured and padded
+@pytest.mark.parametrize("warm", [False, True])
+@pytest.mark.parametrize("i8", [False, True])
+def test_attention_block_captured_and_padded(cr, i8, warm):
+    """A prompt and a token step of ConvRotAttention as captured graphs, with and
+    without calls before the capture, over batches padded to a fixed size:
+    replays with other tokens, pages and lengths are the eager calls' bits."""
+    Hq, Hkv, D, hidden, page, rows = 8, 2, 128, 512, 16, 256
+    W = [randn(160 + i, n, hidden, std=0.05) for i, n in enumerate((Hq * D, Hkv * D, Hkv * D))]
+    Wo = randn(163, hidden, Hq * D, std=0.05)
+
+    def layer():
+        return cr.ConvRotAttention(*W, Wo, q_heads=Hq, kv_heads=Hkv, rope=cr.rope_table(300, D, device="cuda"),
+                                   norm_w=torch.zeros(hidden).cuda())
+
+    def batch(seed, lens):
+        """Tokens of whole prompts padded to `rows`, and one token each padded to 8."""
+        g = torch.Generator().manual_seed(seed)
+        need = [-(-(n + 1) // page) for n in lens]
+        perm, at = torch.randperm(40, generator=g).int(), 0
+        table = torch.full((8, 16), -1, dtype=torch.int32)
+        for i, n in enumerate(need):
+            table[i, :n], at = perm[at:at + n], at + n
+        pad = rows - sum(lens)
+        seq = torch.cat([torch.repeat_interleave(torch.arange(len(lens)), torch.tensor(lens)), torch.full((pad,), -1)])
+        pos = torch.cat([torch.arange(n) for n in lens] + [torch.zeros(pad, dtype=torch.int64)]).int()
+        cu = torch.tensor([0] + lens + [0] * (8 - len(lens))).cumsum(0).int()
+        n = torch.tensor(lens + [0] * (8 - len(lens)), dtype=torch.int32)
+        live = torch.arange(8) < len(lens)
+        s = cr.PagedKVCache.slots
+        cache = cr.PagedKVCache.__new__(cr.PagedKVCache)
+        cache.page_size = page
+        b = dict(x=randn(seed, rows, hidden).cpu(), cu=cu, pos=pos, slots=s(cache, table, seq, pos), x1=randn(seed + 1, 8, hidden).cpu(),
+                 pos1=n, slots1=s(cache, table, torch.where(live, torch.arange(8), -1), n), table=table,
+                 lens1=torch.where(live, n + 1, 0).int())
+        return {k: t.cuda() for k, t in b.items()}
+
+    def step(layer, cache, b):
+        return (layer.prompt(b["x"], b["cu"], b["pos"], b["slots"], cache),
+                layer.decode(b["x1"], b["pos1"], b["slots1"], cache, b["table"], b["lens1"]))
+
+    batches = [(200, [70, 3, 129]), (300, [1]), (400, [17, 16, 15, 40, 100, 1, 2])]
+    eager, want = layer(), []
+    for seed, lens in batches:
+        cache = cr.PagedKVCache(40, Hkv, D, page_size=page, int8=i8)
+        y, y1 = step(eager, cache, batch(seed, lens))
+        assert torch.isfinite(y[:sum(lens)]).all() and torch.isfinite(y1).all() and not y1[len(lens):].any()
+        want.append((y, y1, cache))
+    mine, held = layer(), batch(*batches[0])
+    cache = cr.PagedKVCache(40, Hkv, D, page_size=page, int8=i8)
+    if warm:
+        step(mine, cache, held)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step(mine, cache, held)
+    for i in (2, 0, 1, 2):
+        for t in (cache.k, cache.v, cache.k_scale, cache.v_scale):
+            if t is not None:
+                t.zero_()
+        for k, t in batch(*batches[i]).items():
+            held[k].copy_(t)
+        graph.replay()
+        n = sum(batches[i][1])
+        assert torch.equal(out[0][:n], want[i][0][:n]) and torch.equal(out[1], want[i][1])
+        assert torch.equal(cache.k, want[i][2].k) and torch.equal(cache.v, want[i][2].v)
+    assert cr.convrot_device_status() == 0
+
+
+@pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("D,rot", [(64, 48), (128, 48), (128, 80), (128, 112)])
+def test_append_rotation_widths_between(cr, D, rot, i8):
+    """Widths that end inside a lane's share of the head."""
+    c = append_case(D + rot, 50, 6, 3, D, rot, 48, i8, True, pad=7)
+    before, q, k = run_append(cr, c)
+    check_append(c, before, q, k)
+
+
+def test_rows_far_apart(cr):
+    """Row strides with which offsets pass 2^32 elements: the bits of the same
+    rows side by side."""
+    T, stride, Hq, Hkv, D = 1030, 1 << 22, 8, 2, 128
+    if torch.cuda.mem_get_info()[0] < 24 << 30:
+        pytest.skip("needs 24 GB")
+    big = torch.empty(T * stride, dtype=torch.bfloat16, device="cuda")
+    q, k, v, out = (big.as_strided((T, h, D), (stride, D, 1), at) for h, at in ((Hq, 0), (Hkv, 2048), (Hkv, 4096), (Hq, 8192)))
+    near = [randn(20 + i, *x.shape) for i, x in enumerate((q, k, v))]
+    for x, y in zip((q, k, v), near):
+        x.copy_(y)
+    cu = torch.tensor([0, 500, T], dtype=torch.int32).cuda()
+    assert torch.equal(cr.convrot_attention_prompt(q, k, v, cu, out=out), cr.convrot_attention_prompt(*near, cu))
+    rope, pos = cr.rope_table(T, D, device="cuda"), torch.arange(T, dtype=torch.int32).cuda()
+    slots = torch.randperm(70 * 16, generator=torch.Generator().manual_seed(1))[:T].cuda()
+    caches = [cr.PagedKVCache(70, Hkv, D, page_size=16) for _ in range(2)]
+    far = cr.convrot_rope_append(q, k, v, rope, pos, slots, caches[0].k, caches[0].v, q_out=out)[0]
+    assert torch.equal(far, cr.convrot_rope_append(*near, rope, pos, slots, caches[1].k, caches[1].v)[0])
+    assert torch.equal(caches[0].k, caches[1].k) and torch.equal(caches[0].v, caches[1].v)
+    g = torch.Generator().manual_seed(2)
+    table = torch.randint(0, 70, (T, 3), generator=g, dtype=torch.int32).cuda()
+    lens = torch.randint(0, 49, (T,), generator=g, dtype=torch.int32).cuda()
+    args = caches[0].k, caches[0].v, table, lens
+    assert torch.equal(cr.convrot_attention_decode(q, *args, out=out), cr.convrot_attention_decode(near[0], *args))
+    assert cr.convrot_device_status() == 0

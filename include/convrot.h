@@ -360,7 +360,12 @@ convrot_status convrot_w4a8_gemm_s32(const int8_t* Xq, const uint8_t* Wq4, int M
  * A paged cache is k_cache, v_cache [pages, kv_heads, page_size, D],
  * contiguous, page_size a multiple of 16 up to 4096: bf16 (k_scale = v_scale =
  * NULL), or int8 codes with fp32 scales [pages, kv_heads, page_size] (value =
- * code * scale; scale = max|row| / 127 over the D elements of a token's head).
+ * code * scale; scale = max|row| / 127 over the D elements of a token's head,
+ * never negative).
+ *
+ * Sums over the keys are held in fp32 before they are divided by the
+ * probabilities' sum, which may be up to 2^8 per key: values above about 2^120 /
+ * keys in size may give infinities.
  *
  * Positions, slots, page numbers, lengths and offsets are read on the device.
  * One outside its tensor is never followed, and convrot_device_status reports it
@@ -404,8 +409,10 @@ convrot_status convrot_rope_append(const void* q, int64_t q_stride, const void* 
 /*
  * Attention over whole prompts, packed one after another:
  *   o_i = sum_j softmax_j(scale * q_i . k_j) v_j
- * over the keys j of the row's own sequence; causal != 0: row i of lq sees
- * keys j <= i + lk - lq (the last row sees all).  A row that sees no key is 0.
+ * over the keys j of the row's own sequence, all of them rows of k and v (a
+ * prompt that continues what a cache holds needs those rows there, too);
+ * causal != 0: row i of lq sees keys j <= i + lk - lq (the last row sees all).
+ * A row that sees no key is 0.
  * What a row does not see never reaches it, infinities and NaN included.
  * q [tokens, q_heads, D]; k, v [kv_tokens, kv_heads, D]  in
  * cu_q, cu_k int32 [seqs + 1]  in   non-decreasing offsets of the sequences'
@@ -428,6 +435,8 @@ convrot_status convrot_attention_prompt(const void* q, int64_t q_stride, const v
  * own key and value already appended):
  *   o_b = sum_{j < lens[b]} softmax_j(scale * q_b . k_j) v_j;  0 when lens[b] = 0
  * Key j of sequence b is row j % page_size of page table[b][j / page_size].
+ * Groups of more than 16 query heads per key/value head stream the cache once
+ * for every 16.
  * q [seqs, q_heads, D]  in
  * table      int32 [seqs, table_cols], rows table_stride apart  in  entries
  *            past a sequence's last page are not read

@@ -853,7 +853,9 @@ class ConvRotAttention:
 
     def prompt(self, x: torch.Tensor, cu_seqlens: torch.Tensor, positions: torch.Tensor, slots: torch.Tensor,
                cache: PagedKVCache) -> torch.Tensor:
-        """Whole prompts, packed one after another: x bf16 [tokens, hidden]."""
+        """Whole prompts, packed one after another: x bf16 [tokens, hidden].  A token
+        sees the tokens of its prompt in this call, not what the cache held
+        before.  Rows behind the last prompt (padding) hold nothing of use."""
         q, k, v = self._append(x, positions, slots, cache, True)
         return self.o(convrot_attention_prompt(q, k, v, cu_seqlens, scale=self.scale).flatten(1))
 

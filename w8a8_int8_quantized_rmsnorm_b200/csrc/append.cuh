@@ -18,11 +18,12 @@
 // keeps its token's cosines and sines in registers and walks over the token's
 // head rows, APPEND_UNROLL row groups in flight at a time.
 //
-// Bound by memory: 8192 tokens x (32 + 8 + 8) x 128 in bf16, 222 MB read and
-// written, take 37.2 us (5.97 TB/s, 0.91 of a copy's rate); one token takes 2.1
-// us.  Behind that stands the start of a warp (position and slot, then the
-// table's row, then the head rows): 5035 tokens with both norms take 32 us
-// (0.71), 1.7 waves of warps.  Measured slower there: a token split over more
+// Bound by memory: 8192 tokens x (32 + 8 + 8) x 128 in bf16, 223 MB read and
+// written, take 36.6 us (6.08 TB/s, 0.93 of a copy's rate; graph replays); one
+// token takes 1.9 us, 256 with norms into int8 caches 5.0.  Behind that stands
+// the start of a warp (position and slot, then the table's row, then the head
+// rows): 5035 tokens with both norms take 31 us (0.74), 1.7 waves of warps.
+// Measured slower there: a token split over more
 // warps (36, 40 and 51 us with 64, 128 and 256 warps per SM asked for), the norm
 // weights kept in registers (44 us: 130 registers leave 12 warps per SM).
 #pragma once

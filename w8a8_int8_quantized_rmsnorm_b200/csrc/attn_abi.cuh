@@ -126,7 +126,7 @@ convrot_status run_prompt(const PromptArgs& args, cudaStream_t st) {
   return launch_pdl(k, dim3(grid), dim3(PROMPT_THREADS), smem, st, 1, mq, mk, mv, mo, a);
 }
 
-// Heads of a decode unit: up to eight together, else sixteen at a time.
+// Heads of a decode unit: a group of up to sixteen together, else sixteen at a time.
 int decode_unit_heads(int q_heads, int kv_heads) { return std::min(q_heads / kv_heads, 16); }
 
 constexpr int kDecodeCtas = 2;  // most CTAs per SM of any decode kernel
@@ -370,7 +370,7 @@ convrot_status convrot_attention_decode(const void* q, int64_t q_stride, int seq
   cudaStream_t st = as_cuda(stream);
 #define CONVROT_DECODE(D, I8, NQ) run_decode<D, I8, NQ>(a, k_cache, v_cache, blocks, st)
   // heads of a unit: one 8-column tile takes eight (bf16) or four (int8, in
-  // two columns each); fewer tiles leave registers for more CTAs per SM
+  // two columns each); fewer tiles take fewer registers and instructions
   if (head_dim == 128) {
     if (i8) return h > 8 ? CONVROT_DECODE(128, true, 16) : h > 4 ? CONVROT_DECODE(128, true, 8) : CONVROT_DECODE(128, true, 4);
     return h > 8 ? CONVROT_DECODE(128, false, 16) : CONVROT_DECODE(128, false, 8);

@@ -11,8 +11,8 @@
 // the workspace, and the part that comes last, found by a counter, joins all
 // of them in the order of the keys, so the result does not depend on timing.
 //
-// Inside a CTA one warp fetches (the block table's entries one block ahead,
-// then one TMA box per page piece, into a ring of blocks) and four warps
+// Inside a CTA one warp fetches (the block table's entries a batch of blocks
+// ahead, then one TMA box per page piece, into a ring of blocks) and four warps
 // compute, each 16 keys of a block (32 of int8), on warp-level matrix instructions with the
 // keys as rows and the heads as columns: S^T = K Q^T and O^T += V^T P^T, so a
 // group of four or eight heads fills the 8-column operand and every score
@@ -29,18 +29,24 @@
 // q = s (256 hi + lo) with s = max|q| / 32512, and hi and lo are two columns of
 // one s8 x s8 -> s32 product; probabilities times value scales become the same,
 // of the largest among a warp's 32 keys, and their sum joins the fp32 result.
-// The integer sums are exact.  The query is off by at most 2^-16 of its largest
-// element, which moves a score by scale 2^-16 max|q| sum|k| at most; a
-// probability by 2^-16 of the largest beside it, where bf16 would be off by up
-// to 2^-8 of itself.
+// The integer sums are exact.  The query is off by at most half a step, 1/65024
+// of its largest element, which moves a score by scale max|q| sum|k| / 65024 at
+// most; a probability times its scale by 1/65024 of the largest beside it, where
+// bf16 would be off by up to 2^-8 of itself.  Scales are taken to be 0 or more.
 //
-// Measured (32 query heads on 8, D = 128): 64 contexts of 1 .. 8192 keys, 1.2 GB of
-// bf16, 185 us (6.50 TB/s, 0.99 of a copy's rate); 128 such contexts in int8,
-// 1.14 GB, 177 us (0.98); one context of 131071, 94 us (0.87: about 8 us go into
-// finding the stretch, the first fetch and the join of 37 parts per head); one
-// of 777, 11 us, those alone.  The batches of pages matter: with the block
-// table read one block ahead the int8 stream took 231 us, each block waiting
-// for a table entry that the stream itself had driven out of L2.
+// Measured (32 query heads on 8, D = 128; graph replays): 64 contexts of 1 .. 8192
+// keys, 1.2 GB of bf16, 183 us (6.56 TB/s, a copy's rate); 128 such contexts in
+// int8, 1.14 GB, 176 us (6.48 TB/s, 0.99); one context of 131071, 93 us (0.88:
+// about 8 us go into finding the stretch, the first fetch and the join of 37
+// parts per head); one of 777, 10.7 us, those alone.  The batches of pages
+// matter: with the block table read one block ahead the int8 stream took 231 us,
+// each block waiting for a table entry that the stream itself had driven out of L2.
+//
+// Groups above 8 heads are slower: the second tile of columns spills (100 to 230
+// bytes a thread) and leaves two ring slots.  64 such contexts with groups of 16
+// on 8: bf16 238 us (5.07 TB/s), int8 205 us (3.05 TB/s).  Above 16 heads a unit
+// takes 16 at a time and the cache is streamed once for each: 128 such contexts
+// with 32 heads on one, 0.28 GB once, 111 us; 128 on one, 364 us.
 //
 // Rows past a sequence's end are never used: their scores are replaced, their
 // values' registers cleared, pages behind the last one not fetched.  Neither is
@@ -94,7 +100,7 @@ constexpr unsigned BLOCK_FIRST = 256, BLOCK_LAST = 512, BLOCK_END = 1024;
 template <int D, bool I8, int NQ>
 struct DecodeSmem {
   static constexpr int ESZ = I8 ? 1 : 2;
-  static constexpr int CTAS = 2;               // per SM: between them they keep 200 KB in flight
+  static constexpr int CTAS = 2;               // per SM; a ring holds two blocks (bf16 at D = 128: 64 KB) to six
   static constexpr int KEYS = I8 ? 128 : 64;  // of a block: the same bytes, a multiple of 4 warps x 32 or 16 keys
   static constexpr int TILE = KEYS * D * ESZ;
   static constexpr int SLOT = 2 * TILE;                            // K, V

@@ -15,11 +15,14 @@
 // Work split.  A unit is 2 x 128 query rows of one key/value head: a row is
 // (token, query head of the group), so a group's heads share every key and
 // value tile and a short prompt still fills the matrix unit.  The grid has one
-// CTA per unit, the longest key ranges first; one runs per SM, and when a unit's
-// last copies are under way it takes over the next unit that has not started
+// CTA per unit, from the pack's end to its front, so that of a sequence the
+// units with the most keys come first; one runs per SM, and when a unit's last
+// copies are under way it takes over the next unit that has not started
 // (clusterlaunchcontrol.try_cancel) instead of ending: a pack of very different
-// lengths spreads evenly, and set-up, fetch and store of neighbouring units
-// overlap.  Warps 0-3 and 4-7 each own one 128-row tile (a thread owns a row; no
+// lengths spreads evenly, and a unit's results are stored while the next one
+// runs.  The next unit is asked for behind this one's last copy, so what a change
+// of units costs shows where units are of one or two key tiles.
+// Warps 0-3 and 4-7 each own one 128-row tile (a thread owns a row; no
 // exchange between threads), warp 8 fetches by TMA and announces units, warp 9
 // issues the matrix products.  While one tile's softmax runs, the tensor core
 // works on the other's S or O.
@@ -27,32 +30,39 @@
 // Tensor memory: S0, S1 (128 columns each; P overwrites its own S), O0, O1.
 // Shared memory: the two Q tiles and a ring of K and V tiles (128 keys).
 //
-// Measured (32 query heads on 8, D = 128, causal): 8192 tokens 491 us = 1.12
-// PFLOP/s (0.69 of cuBLAS's burst rate), 2048 tokens 41 us (256 units on 148
-// SMs), 34 prompts of 16 .. 300 tokens 43 us, 2.7 TB/s.  With D = 64, groups of 8
-// and 12 prompts of 1 .. 1333: 77 us.
+// Measured (32 query heads on 8, D = 128, causal; graph replays): 8192 tokens 417
+// us at 1965 MHz (1.32 PFLOP/s, 0.81 of cuBLAS's burst rate), 487 us one after
+// another under the power cap at 1580 MHz (0.82 of its sustained rate); 2048
+// tokens 35 us on inputs that L2 still holds, 37 us on others, 39 us under the
+// cap; 34 prompts of 16 .. 300 tokens 42 us, 2.8 TB/s.  With D = 64, groups of 8 and
+// 12 prompts of 1 .. 1333: 76 us.
 //
-// What bounds a long prompt is the round of one row tile, 3300 cycles: scores
-// (590: both operands come from shared memory, 8 KB per 64 cycles, its whole
+// A key tile of both row tiles takes 3600 cycles (8192 tokens: 225 of them per
+// SM).  Its products need 2050 at the tensor core's rate, its exponentials as
+// many (2 x 128 x 128, 16 a cycle); in 2048 tokens the tensor core is busy for 48 %
+// of the cycles and the exponential unit for 48 %, in the D = 64 pack for 27 % and
+// 53 %.  So no unit is full: what passes is a row tile's chain, from clock stamps
+// scores 590 (both operands come from shared memory, 8 KB per 64 cycles, its whole
 // bandwidth), fetching them 190, maximum 430, 128 exponentials a row 1500, the
-// rest of the product with V 256, and four hand-overs between the issuing warp
-// and the softmax.  The two row tiles take turns; the tensor core needs 2200 of
-// those cycles.  No single part is the limit: without exponentials, maxima and
-// conversions 4096 tokens still took 110 us of 115.  Tensor memory has no room
-// for a third row tile.  Measured no faster: steps of 64 keys with two S buffers
-// (142 us for 4096 tokens: 128 x 64 products are bound by the reads of Q), P
-// apart from S at D = 64 (104 us instead of 99: without turns both tiles reach
-// their exponentials together), a quarter of the exponentials as a cubic on the
-// multiply-add pipe (the same at D = 128, 0.5 % less at D = 64), three ring slots
-// instead of four and room for whole result tiles (525 us for 8192 tokens).
-// Handing units out by cluster launch control instead of a fixed order took the
-// ragged pack from 103 to 81 us.  A short prompt is bound by a unit's chain of
-// set-up, one softmax, product and store, 3.3 us.
+// rest of the product with V 256, and four hand-overs between the issuing warp,
+// which serves the two row tiles in a fixed order, and the softmax.  How much of
+// it the hand-overs and that order are is not settled: without exponentials,
+// maxima and conversions 4096 tokens still took 110 us of 115.
+// Tensor memory has no room for a third row tile.  Measured no faster: steps of
+// 64 keys with two S buffers (142 us for 4096 tokens: 128 x 64 products are bound
+// by the reads of Q), P apart from S at D = 64 (104 us instead of 99: without
+// turns both tiles reach their exponentials together), a quarter of the
+// exponentials as a cubic on the multiply-add pipe (the same at D = 128, 0.5 % less
+// at D = 64), three ring slots instead of four and room for whole result tiles
+// (525 us for 8192 tokens under the cap).  Handing units out by cluster launch
+// control instead of a fixed order took the ragged pack from 103 to 81 us.
 //
 // A probability of zero times an infinite or NaN value is NaN in the matrix
 // unit.  Such a value may sit in a masked place (a later token, the next
 // sequence of the pack, memory behind the last one), so a row whose result
 // holds a NaN is computed again by attention_row over its visible keys alone.
+// That is one warp's work at scalar speed: where every row sees a value with one
+// NaN element, 2048 tokens take 18 ms and 8192 take 246 ms.
 #pragma once
 
 #include "attn_row.cuh"

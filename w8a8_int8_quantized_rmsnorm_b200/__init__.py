@@ -210,7 +210,8 @@ class Workspace:
     It starts zero-filled; the library leaves it zero after every call whose
     kernels complete, so it is reused without clearing.  After
     convrot_device_status has reported a device timeout (an aborted call may
-    leave partial sums behind) it is zero-filled again before its next use.
+    leave partial sums behind) it is zero-filled again before its next use;
+    graphs captured with it before are to be captured again.
     One Workspace must not be used by calls that run concurrently on
     different streams, replays of captured graphs among them.
 
